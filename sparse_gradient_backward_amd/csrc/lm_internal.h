@@ -1,0 +1,220 @@
+// lm_internal.h -- what the token-model operators (lm_*.hip) share: element
+// types and their vector loads, cross-lane reductions, the workspace header,
+// host-side argument helpers.  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "sgb_lm.h"
+
+namespace sgb_lm {
+
+// ---------------------------------------------------------------- workspace
+
+// First bytes of every workspace.  The first error of the call with `epoch`
+// is kept as epoch << 8 | code; a word from another epoch counts as none, so
+// nothing needs clearing between calls.
+struct Header {
+  uint32_t status;
+  uint32_t epoch;
+};
+constexpr size_t kHeaderBytes = 256;
+
+// ---------------------------------------------------------------- elements
+
+using bf16_t = __bf16;
+using f16_t = _Float16;
+
+template <typename T>
+struct Vec {  // eight elements; an element's alignment is enough (the target's
+              // global loads and stores take any byte address)
+  static constexpr int kWords = sizeof(T) * 2;
+  typedef T type __attribute__((ext_vector_type(8)));
+  struct __attribute__((packed, aligned(sizeof(T)))) Mem {
+    uint32_t w[kWords];
+  };
+};
+
+// Eight elements as loaded.
+template <typename T>
+struct Raw8 {
+  uint32_t w[Vec<T>::kWords];
+};
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(bf16_t v) { return (float)v; }
+__device__ __forceinline__ float widen(f16_t v) { return (float)v; }
+
+// Loads p[0 .. n) (n <= 8; nothing for n <= 0); the others are zero.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
+  Raw8<T> r;
+  if (n >= 8) {
+    const typename Vec<T>::Mem m = *reinterpret_cast<const typename Vec<T>::Mem*>(p);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kWords; ++i) r.w[i] = m.w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kWords; ++i) r.w[i] = 0;
+    if (n > 0) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i) {
+        if (i < n) {
+          if constexpr (sizeof(T) == 4) {
+            r.w[i] = __float_as_uint(p[i]);
+          } else {
+            const uint32_t u = reinterpret_cast<const uint16_t*>(p)[i];
+            r.w[i >> 1] |= u << (16 * (i & 1));
+          }
+        }
+      }
+    }
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __uint_as_float(r.w[i]);
+    } else if constexpr (__is_same(T, bf16_t)) {
+      // the 16 bits are the high half of the fp32 word: exact
+      v[i] = __uint_as_float((i & 1) ? (r.w[i >> 1] & 0xffff0000u) : (r.w[i >> 1] << 16));
+    } else {
+      v[i] = (float)__builtin_bit_cast(f16_t, (uint16_t)(r.w[i >> 1] >> (16 * (i & 1))));
+    }
+  }
+}
+
+// Stores v[0 .. n) rounded to T, to nearest even.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
+  typename Vec<T>::type t;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = (T)v[i];
+  if (n >= 8) {
+    *reinterpret_cast<typename Vec<T>::Mem*>(p) = __builtin_bit_cast(typename Vec<T>::Mem, t);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = t[i];
+  }
+}
+
+// Eight elements of a type known at run time (parameters: read once a block).
+__device__ __forceinline__ void load8_as(const void* base, int dtype, int64_t at, int n,
+                                         float (&v)[8]) {
+  if (dtype == SGB_F32)
+    widen8(load8(static_cast<const float*>(base) + at, n), v);
+  else if (dtype == SGB_BF16)
+    widen8(load8(static_cast<const bf16_t*>(base) + at, n), v);
+  else
+    widen8(load8(static_cast<const f16_t*>(base) + at, n), v);
+}
+
+// ---------------------------------------------------------------- wave64
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+
+// Folds x over groups of `width` lanes (8, 16, 32 or 64, wave-uniform); every
+// lane of a group gets the same bits.  Lane exchanges inside the vector unit
+// (data-parallel primitives within a row of 16, then the row and half
+// swaps): six dependent steps of a few cycles each, where a shuffle through
+// LDS takes tens.
+template <typename F>
+__device__ __forceinline__ float wave_fold(float x, int width, F f) {
+  x = f(x, dpp<0xB1>(x));   // lane ^ 1
+  x = f(x, dpp<0x4E>(x));   // lane ^ 2
+  x = f(x, dpp<0x141>(x));  // mirrored in 8
+  if (width > 8) x = f(x, dpp<0x140>(x));  // mirrored in 16
+  if (width > 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    x = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  if (width > 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    x = f(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  return x;
+}
+
+__device__ __forceinline__ float wave_add(float x, int width = 64) {
+  return wave_fold(x, width, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float x, int width = 64) {
+  return wave_fold(x, width, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// Records `code` as the call's error unless it already has one.
+__device__ __forceinline__ void set_status(Header* h, uint32_t epoch, uint32_t code) {
+  uint32_t old = __hip_atomic_load(&h->status, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  while ((old >> 8) != epoch) {
+    const uint32_t seen = atomicCAS(&h->status, old, (epoch << 8) | code);
+    if (seen == old) break;
+    old = seen;
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+uint32_t next_epoch();
+int current_device();  // -1: none; a plan made then checks its calls' arguments, no more
+int compute_units(int device);
+
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = false;
+  explicit DeviceGuard(int dev) {
+    if (dev < 0 || hipGetDevice(&prev) != hipSuccess) return;
+    ok = prev == dev || hipSetDevice(dev) == hipSuccess;
+  }
+  ~DeviceGuard() {
+    if (ok && prev >= 0) (void)hipSetDevice(prev);
+  }
+};
+
+inline size_t align_up(size_t n, size_t a) { return (n + a - 1) / a * a; }
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+inline size_t elem_size(int dtype) { return dtype == SGB_F32 ? 4 : 2; }
+inline bool float_dtype(int dtype) {
+  return dtype == SGB_F32 || dtype == SGB_BF16 || dtype == SGB_F16;
+}
+
+// A matrix argument: there, aligned to its elements, rows that do not overlap.
+inline bool matrix_ok(const void* p, int64_t width, int64_t stride, size_t elem) {
+  return p && aligned(p, elem) && stride >= width && stride <= (1ll << 40);
+}
+
+inline bool workspace_ok(const void* ws) { return ws && aligned(ws, 256); }
+
+// Do the bytes of two row-strided matrices (of `rows` rows, or rows_b the
+// second) share a range?  (Interleaved rows
+// of one buffer, e.g. the halves of wider rows, are told apart by `same
+// stride, disjoint columns`.)
+inline bool overlap(const void* a, int64_t wa, int64_t sa, size_t ea, const void* b, int64_t wb,
+                    int64_t sb, size_t eb, int64_t rows, int64_t rows_b = -1) {
+  if (rows_b < 0) rows_b = rows;
+  if (!a || !b || rows <= 0 || rows_b <= 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uint64_t la = ((uint64_t)(rows - 1) * sa + wa) * ea,
+                 lb = ((uint64_t)(rows_b - 1) * sb + wb) * eb;
+  if (a0 + la <= b0 || b0 + lb <= a0) return false;
+  if (sa * (int64_t)ea != sb * (int64_t)eb || (rows < 2 && rows_b < 2)) return true;
+  const uint64_t pitch = (uint64_t)sa * ea;
+  const uint64_t d = (b0 >= a0 ? b0 - a0 : pitch - (a0 - b0) % pitch) % pitch;
+  // b's columns start d bytes after a's in the shared pitch
+  return !(d >= (uint64_t)wa * ea && d + (uint64_t)wb * eb <= pitch);
+}
+
+}  // namespace sgb_lm
