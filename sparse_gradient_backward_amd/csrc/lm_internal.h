@@ -28,18 +28,15 @@ using bf16_t = __bf16;
 using f16_t = _Float16;
 
 template <typename T>
-struct Vec {  // eight elements; an element's alignment is enough (the target's
-              // global loads and stores take any byte address)
+struct Vec {
   static constexpr int kWords = sizeof(T) * 2;
   typedef T type __attribute__((ext_vector_type(8)));
-  struct __attribute__((packed, aligned(sizeof(T)))) Mem {
-    uint32_t w[kWords];
-  };
 };
 
-// Eight elements as loaded.
+// Eight elements as loaded; an element's alignment is enough (the target's
+// global loads and stores take any byte address).
 template <typename T>
-struct Raw8 {
+struct __attribute__((packed, aligned(sizeof(T)))) Raw8 {
   uint32_t w[Vec<T>::kWords];
 };
 
@@ -52,9 +49,7 @@ template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
   Raw8<T> r;
   if (n >= 8) {
-    const typename Vec<T>::Mem m = *reinterpret_cast<const typename Vec<T>::Mem*>(p);
-#pragma unroll
-    for (int i = 0; i < Vec<T>::kWords; ++i) r.w[i] = m.w[i];
+    r = *reinterpret_cast<const Raw8<T>*>(p);
   } else {
 #pragma unroll
     for (int i = 0; i < Vec<T>::kWords; ++i) r.w[i] = 0;
@@ -73,6 +68,69 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
     }
   }
   return r;
+}
+
+// The same in two parts, for loads that are to be in flight while other work
+// goes on: a branch around a load makes the compiler wait for it where the
+// branch ends.  ask8() loads without one: the eight elements that end at `end`
+// where fewer than eight are left, and zeros from a place of its own where the
+// row is shorter than eight (`row` must hold at least `end` elements).
+// have8() then moves the n elements wanted to the front and clears the rest.
+static __device__ const uint32_t kNowhere[8] = {};
+
+// *p, or `none` for a null pointer (uniform), without a branch.  The address
+// space keeps a selected address out of the generic loads, which wait for LDS
+// too.
+template <typename U>
+__device__ __forceinline__ U load_global(uintptr_t p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  return *reinterpret_cast<const __attribute__((address_space(1))) U*>(p);
+#else
+  return *reinterpret_cast<const U*>(p);  // the host's pass has no such spaces
+#endif
+}
+template <typename U>
+__device__ __forceinline__ U value_or(const U* p, int64_t at, U none) {
+  const U v = load_global<U>(p ? (uintptr_t)(p + at) : (uintptr_t)kNowhere);
+  return p ? v : none;
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> ask8(const T* row, int64_t col, int64_t end) {
+  const bool there = row && end >= 8;  // uniform
+  const uintptr_t p = there ? (uintptr_t)row : (uintptr_t)kNowhere;
+  return load_global<Raw8<T>>(p + (there ? min(col, end - 8) : 0) * sizeof(T));
+}
+
+template <typename T>
+__device__ __forceinline__ void have8(Raw8<T>& r, const T* row, int64_t col, int64_t end, int n) {
+  if (row && end < 8) {  // uniform
+    r = load8(row + col, n);
+  } else if (n < 8) {
+    constexpr int W = Vec<T>::kWords, E = sizeof(T) / 2;  // words, half words an element
+    const int by = 8 - n;
+#pragma unroll
+    for (int step = 4; step >= 1; step >>= 1) {
+      const bool move = by & step;
+      if (step * E >= 2) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const uint32_t next = i + step * E / 2 < W ? r.w[i + step * E / 2] : 0u;
+          r.w[i] = move ? next : r.w[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const uint32_t next = i + 1 < W ? r.w[i + 1] : 0u;
+          r.w[i] = move ? (r.w[i] >> 16 | next << 16) : r.w[i];
+        }
+      }
+    }
+    if (n <= 0) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) r.w[i] = 0;
+    }
+  }
 }
 
 template <typename T>
@@ -97,7 +155,7 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) t[i] = (T)v[i];
   if (n >= 8) {
-    *reinterpret_cast<typename Vec<T>::Mem*>(p) = __builtin_bit_cast(typename Vec<T>::Mem, t);
+    *reinterpret_cast<Raw8<T>*>(p) = __builtin_bit_cast(Raw8<T>, t);
   } else {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
