@@ -72,21 +72,22 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int n) {
 
 // The same in two parts, for loads that are to be in flight while other work
 // goes on: a branch around a load makes the compiler wait for it where the
-// branch ends.  ask8() loads without one: the eight elements that end at `end`
-// where fewer than eight are left, and zeros from a place of its own where the
-// row is shorter than eight (`row` must hold at least `end` elements).
-// have8() then moves the n elements wanted to the front and clears the rest.
+// branch ends.  ask8() loads without one: from `at`, or the eight elements that
+// end at `end` (>= 8) where fewer than eight are left; zeros where there is no
+// row.  have8() then moves the n elements wanted to the front and clears the
+// rest.  `row` is best uniform and `at` the lane's: one scalar base address.
 static __device__ const uint32_t kNowhere[8] = {};
 
 // *p, or `none` for a null pointer (uniform), without a branch.  The address
 // space keeps a selected address out of the generic loads, which wait for LDS
 // too.
 template <typename U>
-__device__ __forceinline__ U load_global(uintptr_t p) {
+__device__ __forceinline__ U load_global(uintptr_t p, uint32_t bytes = 0) {
 #ifdef __HIP_DEVICE_COMPILE__
-  return *reinterpret_cast<const __attribute__((address_space(1))) U*>(p);
+  return *reinterpret_cast<const __attribute__((address_space(1))) U*>(
+      reinterpret_cast<const __attribute__((address_space(1))) char*>(p) + bytes);
 #else
-  return *reinterpret_cast<const U*>(p);  // the host's pass has no such spaces
+  return *reinterpret_cast<const U*>(p + bytes);  // the host's pass has no such spaces
 #endif
 }
 template <typename U>
@@ -96,17 +97,14 @@ __device__ __forceinline__ U value_or(const U* p, int64_t at, U none) {
 }
 
 template <typename T>
-__device__ __forceinline__ Raw8<T> ask8(const T* row, int64_t col, int64_t end) {
-  const bool there = row && end >= 8;  // uniform
-  const uintptr_t p = there ? (uintptr_t)row : (uintptr_t)kNowhere;
-  return load_global<Raw8<T>>(p + (there ? min(col, end - 8) : 0) * sizeof(T));
+__device__ __forceinline__ Raw8<T> ask8(const T* row, uint32_t at, uint32_t end) {
+  return load_global<Raw8<T>>(row ? (uintptr_t)row : (uintptr_t)kNowhere,
+                              (row ? min(at, end - 8) : 0u) * (uint32_t)sizeof(T));
 }
 
 template <typename T>
-__device__ __forceinline__ void have8(Raw8<T>& r, const T* row, int64_t col, int64_t end, int n) {
-  if (row && end < 8) {  // uniform
-    r = load8(row + col, n);
-  } else if (n < 8) {
+__device__ __forceinline__ void have8(Raw8<T>& r, int n) {
+  if (n < 8) {
     constexpr int W = Vec<T>::kWords, E = sizeof(T) / 2;  // words, half words an element
     const int by = 8 - n;
 #pragma unroll
@@ -148,14 +146,26 @@ __device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
   }
 }
 
-// Stores v[0 .. n) rounded to T, to nearest even.
+// Stores v[0 .. n) rounded to T, to nearest even.  Whole vectors go past the
+// caches' own copies (non-temporal): outputs as long as these would only push
+// out what is still to be read (block norms of 8192 x 4096: 82 -> 72 us;
+// penalties on 512 x 131072 fp32: 105 -> 101; sums of 4096 x 131072 logits whose
+// gradient was written before: 214 -> 178).
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
   typename Vec<T>::type t;
 #pragma unroll
   for (int i = 0; i < 8; ++i) t[i] = (T)v[i];
   if (n >= 8) {
-    *reinterpret_cast<Raw8<T>*>(p) = __builtin_bit_cast(Raw8<T>, t);
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    typedef Words Any __attribute__((aligned(2)));
+    constexpr int W = sizeof(T) / 2;
+    struct Quads {
+      Words q[W];
+    };
+    const Quads r = __builtin_bit_cast(Quads, t);
+#pragma unroll
+    for (int i = 0; i < W; ++i) __builtin_nontemporal_store(r.q[i], reinterpret_cast<Any*>(p) + i);
   } else {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
@@ -163,7 +173,7 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
   }
 }
 
-// Eight elements of a type known at run time (parameters: read once a block).
+// Eight elements of a type known at run time.
 __device__ __forceinline__ void load8_as(const void* base, int dtype, int64_t at, int n,
                                          float (&v)[8]) {
   if (dtype == SGB_F32)
@@ -172,6 +182,68 @@ __device__ __forceinline__ void load8_as(const void* base, int dtype, int64_t at
     widen8(load8(static_cast<const bf16_t*>(base) + at, n), v);
   else
     widen8(load8(static_cast<const f16_t*>(base) + at, n), v);
+}
+
+// The same in two parts, as above (`width`
+// >= 8, unless `tiny`: then all is left to have8_as).
+struct RawAs {
+  uint32_t w[8];
+};
+struct __attribute__((packed, aligned(2))) Four {
+  uint32_t w[4];
+};
+
+template <bool TINY = false>
+__device__ __forceinline__ RawAs ask8_as(const void* base, int dtype, int64_t col, int64_t width) {
+  RawAs r{};
+  if (TINY) return r;
+  const uintptr_t p = base ? (uintptr_t)base + (dtype == SGB_F32 ? 4 : 2) * min(col, width - 8)
+                           : (uintptr_t)kNowhere;
+  const Four lo = load_global<Four>(p), hi = load_global<Four>(p + (dtype == SGB_F32 ? 16 : 0));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.w[i] = lo.w[i], r.w[4 + i] = hi.w[i];
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen_as(const RawAs& r, float (&v)[8]) {
+  Raw8<T> x;
+#pragma unroll
+  for (int i = 0; i < Vec<T>::kWords; ++i) x.w[i] = r.w[i];
+  widen8(x, v);
+}
+
+// `none` for all of them where there is no array.
+template <bool TINY = false>
+__device__ __forceinline__ void have8_as(const RawAs& r, const void* base, int dtype, int64_t col,
+                                         int n, float none, float (&v)[8]) {
+  if (!base) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = none;
+    return;
+  }
+  if (TINY) {
+    load8_as(base, dtype, col, n, v);
+    return;
+  }
+  if (dtype == SGB_F32)
+    widen_as<float>(r, v);
+  else if (dtype == SGB_BF16)
+    widen_as<bf16_t>(r, v);
+  else
+    widen_as<f16_t>(r, v);
+  if (n < 8) {
+#pragma unroll
+    for (int step = 4; step >= 1; step >>= 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float next = i + step < 8 ? v[i + step] : 0.f;
+        v[i] = (8 - n) & step ? next : v[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = n > 0 ? v[i] : 0.f;
+  }
 }
 
 // ---------------------------------------------------------------- wave64

@@ -22,18 +22,25 @@ namespace {
 constexpr int kMaxCols = 8192;
 constexpr int kMaxWaves = 16;
 
+// Team shapes: rows of fewer than eight columns (a load of eight does not fit
+// in them); a team narrower than a wave; 1 to 8 waves; 16 waves (rows of more
+// than 4096 columns, in workgroups of 1024).
+enum Shape { kTiny, kNarrow, kWide, kWhole };
+template <int S>
+constexpr int kThreads = S == kWhole ? 1024 : 512;
+
 // ------------------------------------------------------------- team sums
 
 // Sums each of v[NV] over the team.  `lds` holds 2 * NV_MAX * kMaxWaves
 // floats; successive calls use its halves in turn (`phase`), so that one
 // barrier a call is enough: a half is written again only after the barrier of
 // the call in between.  Contains a barrier if tpr > 64 (block-uniform).
-template <int NV>
+template <int S, int NV>
 __device__ __forceinline__ void team_sum(float (&v)[NV], int tpr, float* lds, int& phase) {
-  const int in_wave = tpr < 64 ? tpr : 64;
+  const int in_wave = S <= kNarrow ? tpr : 64;
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i] = wave_add(v[i], in_wave);
-  if (tpr <= 64) return;
+  if (S <= kNarrow || tpr == 64) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = tpr >> 6;
   float* half = lds + phase * (2 * kMaxWaves);
   phase ^= 1;
@@ -54,6 +61,7 @@ __device__ __forceinline__ void team_sum(float (&v)[NV], int tpr, float* lds, in
 // Mean and 1 / deviation of the team's row.  The layer norm's variance is the
 // mean squared distance from the mean (a second sum over the registers):
 // E[v^2] - E[v]^2 loses what matters when the mean is large.
+template <int S>
 __device__ __forceinline__ void row_stats(const float (&v)[8], int n, int kind, float inv_d,
                                           float eps, int tpr, float* lds, int& phase, float& mean,
                                           float& rs) {
@@ -65,7 +73,7 @@ __device__ __forceinline__ void row_stats(const float (&v)[8], int n, int kind, 
     s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[0] += v[i];
-    team_sum(s, tpr, lds, phase);
+    team_sum<S>(s, tpr, lds, phase);
     mean = s[0] * inv_d;
   }
   s[0] = 0.f;
@@ -74,7 +82,7 @@ __device__ __forceinline__ void row_stats(const float (&v)[8], int n, int kind, 
     const float d = i < n ? v[i] - mean : 0.f;
     s[0] = fmaf(d, d, s[0]);
   }
-  team_sum(s, tpr, lds, phase);
+  team_sum<S>(s, tpr, lds, phase);
   rs = 1.0f / sqrtf(fmaf(s[0], inv_d, eps));
 }
 
@@ -85,28 +93,26 @@ struct Params {  // of the two norms
   float post_eps, pre_eps, scale;
 };
 
-__device__ __forceinline__ void load_param(const void* p, int dtype, int col, int n, float fill,
-                                           float (&v)[8]) {
-  if (p) {
-    load8_as(p, dtype, col, n, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fill;
-  }
+// A row's loads, of which kTiny's are made when they are needed.
+template <int S, typename T>
+__device__ __forceinline__ Raw8<T> ask_row(const T* row, int64_t col, int64_t width) {
+  if (S == kTiny) return Raw8<T>{};
+  return ask8(row, col, width);
 }
-
-// Team shapes: a team narrower than a wave; 1 to 8 waves; 16 waves (rows of
-// more than 4096 columns, in workgroups of 1024).
-enum Shape { kNarrow, kWide, kWhole };
-template <int S>
-constexpr int kThreads = S == kWhole ? 1024 : 512;
+template <int S, typename T>
+__device__ __forceinline__ void have_row(Raw8<T>& r, const T* row, int64_t col, int n) {
+  if (S == kTiny)
+    r = load8(row + col, row ? n : 0);
+  else
+    have8(r, n);
+}
 
 // This thread's team in the workgroup.  From a wave up it is the same for all
 // lanes; saying so keeps row numbers and addresses in scalar registers.
 template <int S>
 __device__ __forceinline__ int team_in_block(int tpr) {
   const int t = (int)threadIdx.x / tpr;
-  return S == kNarrow ? t : __builtin_amdgcn_readfirstlane(t);
+  return S <= kNarrow ? t : __builtin_amdgcn_readfirstlane(t);
 }
 
 // ------------------------------------------------------------- forward
@@ -136,37 +142,49 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_forward(FwdArgs a) {
 
   Raw8<T> rh, rg;
   Raw8<R> rx;
+  // without branches, so that nothing waits for these loads before the values
+  // are used; rows past the last load it again
   auto fetch = [&](int64_t row) {
-    const int64_t g = gate ? row / a.rpg : 0;
-      const int m = row < a.rows ? n : 0;
-      rh = load8(h + row * a.sh + col, m);
-      rx = load8(x + row * a.sx + col, m);
-      if (gate) rg = load8(gate + g * a.sg + col, m);
+    const uint32_t r = (uint32_t)min(row, a.rows - 1);
+    rh = ask_row<S>(h + r * a.sh, col, D);
+    rx = ask_row<S>(x + r * a.sx, col, D);
+    rg = ask_row<S>(gate ? gate + (int64_t)(r / (uint32_t)a.rpg) * a.sg : gate, col, D);
+  };
+  auto have = [&](int64_t row) {
+    const uint32_t r = (uint32_t)min(row, a.rows - 1);
+    have_row<S>(rh, h + r * a.sh, col, n);
+    have_row<S>(rx, x + r * a.sx, col, n);
+    have_row<S>(rg, gate ? gate + (int64_t)(r / (uint32_t)a.rpg) * a.sg : gate, col, n);
   };
   fetch(team);
+  constexpr bool TINY = S == kTiny;
   float pw[8], pb[8], qw[8], qb[8];
-  load_param(a.p.post_w, a.p.dtype, col, n, 1.f, pw);
-  load_param(a.p.post_b, a.p.dtype, col, n, 0.f, pb);
-  load_param(a.p.pre_w, a.p.dtype, col, n, 1.f, qw);
-  load_param(a.p.pre_b, a.p.dtype, col, n, 0.f, qb);
+  const int pt = a.p.dtype;
+  const RawAs rpw = ask8_as<TINY>(a.p.post_w, pt, col, D), rpb = ask8_as<TINY>(a.p.post_b, pt, col, D),
+              rqw = ask8_as<TINY>(a.p.pre_w, pt, col, D), rqb = ask8_as<TINY>(a.p.pre_b, pt, col, D);
+  have8_as<TINY>(rpw, a.p.post_w, pt, col, n, 1.f, pw);
+  have8_as<TINY>(rpb, a.p.post_b, pt, col, n, 0.f, pb);
+  have8_as<TINY>(rqw, a.p.pre_w, pt, col, n, 1.f, qw);
+  have8_as<TINY>(rqb, a.p.pre_b, pt, col, n, 0.f, qb);
 
   int phase = 0;
   // every team of the block makes the same number of turns: the sums' barriers
-  const int64_t turns = (a.rows - (int64_t)blockIdx.x * in_block + a.teams - 1) / a.teams;
-  for (int64_t k = 0; k < turns; ++k) {
+  const uint32_t turns =
+      ((uint32_t)(a.rows - (int64_t)blockIdx.x * in_block) - 1) / (uint32_t)a.teams + 1;
+  for (uint32_t k = 0; k < turns; ++k) {
     const int64_t row = team + k * a.teams;
     float v[8], xo[8], g[8];
-      widen8(rh, v);
-      widen8(rx, xo);
-      if (gate) {
-        widen8(rg, g);
-      } else {
+    have(row);
+    widen8(rh, v);
+    widen8(rx, xo);
+    widen8(rg, g);
+    if (!gate) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = 1.f;
-      }
+      for (int i = 0; i < 8; ++i) g[i] = 1.f;
+    }
     if (k + 1 < turns) fetch(row + a.teams);
     float mh, rsh, mx, rsx;
-    row_stats(v, n, a.p.post, inv_d, a.p.post_eps, tpr, lds, phase, mh, rsh);
+    row_stats<S>(v, n, a.p.post, inv_d, a.p.post_eps, tpr, lds, phase, mh, rsh);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float z = fmaf((v[i] - mh) * rsh, pw[i], pb[i]);
@@ -176,7 +194,7 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_forward(FwdArgs a) {
       }
     const bool on = row < a.rows;
       store8(static_cast<R*>(a.x_out) + row * a.sxo + col, xo, on ? n : 0);
-    row_stats(xo, n, a.p.pre, inv_d, a.p.pre_eps, tpr, lds, phase, mx, rsx);
+    row_stats<S>(xo, n, a.p.pre, inv_d, a.p.pre_eps, tpr, lds, phase, mx, rsx);
     if (a.y) {
         float y[8];
 #pragma unroll
@@ -235,7 +253,9 @@ struct BwdArgs {
   int use_h;
 };
 
-template <typename T, typename R, int S, bool GROUPED, bool BIAS>
+// FULL: a bias's gradient is wanted or a norm subtracts its mean (a layer norm);
+// without it the two rms norms need neither the means nor half of the sums.
+template <typename T, typename R, int S, bool GROUPED, bool FULL>
 __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   __shared__ float lds[4 * kMaxWaves];
   constexpr int NT = kThreads<S>;
@@ -246,14 +266,16 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   const int64_t team = (int64_t)blockIdx.x * in_block + team_in_block<S>(tpr);
   const int col = t * 8, n = min(8, D - col);
   int64_t r0, r1, g0;  // the team's rows; its (first) gate row
+  // (rows, teams and gates are below 2^31: 32-bit divisions)
   if (a.d.split) {
-    g0 = team / a.d.k;
-    r0 = g0 * a.rpg + team % a.d.k * a.d.rp;
+    const uint32_t group = (uint32_t)team / (uint32_t)a.d.k;
+    g0 = group;
+    r0 = g0 * a.rpg + ((uint32_t)team - group * (uint32_t)a.d.k) * a.d.rp;
     r1 = min(min(r0 + a.d.rp, (g0 + 1) * a.rpg), a.rows);
   } else {
     r0 = team * a.d.rp;
     r1 = min(r0 + a.d.rp, a.rows);
-    g0 = a.gate ? r0 / a.rpg : 0;
+    g0 = a.gate ? (uint32_t)min(r0, a.rows) / (uint32_t)a.rpg : 0;
   }
   if (team >= a.d.teams) r1 = r0 = 0;
   const float inv_d = 1.0f / (float)D;
@@ -266,27 +288,43 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   Raw8<R> rdxo, rx;
   Raw8<T> rdy, rh, rg;
   float4 st;
+  auto at_row = [&](int64_t row) { return min(row, a.rows - 1); };
+  auto at_gate = [&](int64_t g) { return GROUPED ? gate + min(g, a.d.groups - 1) * a.sg : gate; };
+  // without branches, as in the forward; rows past the team's are cleared
   auto fetch = [&](int64_t row, int64_t g) {
-    const bool on = row < r1;
-    st = on ? *reinterpret_cast<const float4*>(a.stats + row * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const int m = on ? n : 0;
-      rdxo = load8(dxo + row * a.sdxo + col, m);
-      rdy = load8(dy + row * a.sdy + col, dy ? m : 0);
-      rx = load8(x + row * a.sx + col, dy ? m : 0);
-      rh = load8(h + row * a.sh + col, a.use_h ? m : 0);
-      if (GROUPED) rg = load8(gate + g * a.sg + col, m);
+    const int64_t r = at_row(row);
+    st = load_global<float4>((uintptr_t)(a.stats + r * 4));
+    rdxo = ask_row<S>(dxo + r * a.sdxo, col, D);
+    rdy = ask_row<S>(dy ? dy + r * a.sdy : dy, col, D);
+    rx = ask_row<S>(dy ? x + r * a.sx : (const R*)nullptr, col, D);
+    rh = ask_row<S>(a.use_h ? h + r * a.sh : (const T*)nullptr, col, D);
+    if (GROUPED) rg = ask_row<S>(at_gate(g), col, D);
+  };
+  auto have = [&](int64_t row, int64_t g) {
+    const int64_t r = at_row(row);
+    const int m = row < r1 ? n : 0;
+    have_row<S>(rdxo, dxo + r * a.sdxo, col, m);
+    have_row<S>(rdy, dy ? dy + r * a.sdy : dy, col, m);
+    have_row<S>(rx, dy ? x + r * a.sx : (const R*)nullptr, col, m);
+    have_row<S>(rh, a.use_h ? h + r * a.sh : (const T*)nullptr, col, m);
+    if (GROUPED) have_row<S>(rg, at_gate(g), col, m);
   };
   fetch(r0, g0);
+  constexpr bool TINY = S == kTiny;
   float pw[8], pb[8], qw[8], gt[8];
-  load_param(a.p.post_w, a.p.dtype, col, n, 1.f, pw);
-  load_param(BIAS ? a.p.post_b : nullptr, a.p.dtype, col, n, 0.f, pb);
-  load_param(a.p.pre_w, a.p.dtype, col, n, 1.f, qw);
+  const int pt = a.p.dtype;
+  const void* post_b = FULL ? a.p.post_b : nullptr;
+  const RawAs rpw = ask8_as<TINY>(a.p.post_w, pt, col, D), rpb = ask8_as<TINY>(post_b, pt, col, D),
+              rqw = ask8_as<TINY>(a.p.pre_w, pt, col, D);
   if (gate && !GROUPED) {
     widen8(load8(gate + g0 * a.sg + col, r0 < r1 ? n : 0), gt);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) gt[i] = 1.f;
   }
+  have8_as<TINY>(rpw, a.p.post_w, pt, col, n, 1.f, pw);
+  have8_as<TINY>(rpb, post_b, pt, col, n, 0.f, pb);
+  have8_as<TINY>(rqw, a.p.pre_w, pt, col, n, 1.f, qw);
   // A workgroup of 16 waves has 128 registers a lane: the parameters wait in
   // LDS there, each lane's own columns, and are read back where they are used
   // (in registers they cost over a hundred spills a lane).
@@ -309,7 +347,7 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   put_by(0, qw);
   put_by(1, pw);
   if (!GROUPED) put_by(2, gt);
-  if (BIAS) put_by(3, pb);
+  if (FULL) put_by(3, pb);
   if (IN_LDS) __syncthreads();
 
   float A[8] = {}, B[8] = {}, P[8] = {}, Q[8] = {}, C[8] = {}, E[8] = {};
@@ -319,7 +357,8 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
     const int64_t row = r0 + k;
     const bool on = row < r1;
     float dyv[8], u[8], v[8], tv[8];
-    const float mh = st.x, rsh = st.y, mx = st.z, rsx = st.w;
+    const float mh = FULL ? st.x : 0.f, rsh = st.y, mx = FULL ? st.z : 0.f, rsx = st.w;
+    have(row, g);
       widen8(rdxo, tv);
       widen8(rdy, dyv);
       widen8(rx, u);
@@ -329,19 +368,19 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
     if (k + 1 < a.d.rp) fetch(row + 1, GROUPED && left == 1 ? g + 1 : g);
 
     if (dy) {
-      float s[2] = {0.f, 0.f};
+      float s[1 + FULL] = {};
       get_by(0, qw);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           u[i] = (u[i] - mx) * rsx;
           const float d = dyv[i], w = d * qw[i];
           s[0] = fmaf(w, u[i], s[0]);
-          s[1] += w;
+          if constexpr (FULL) s[1] += w;
           C[i] = fmaf(d, u[i], C[i]);
-          if (BIAS) E[i] += d;
+          if (FULL) E[i] += d;
         }
-      team_sum(s, tpr, lds, phase);
-      const float m1 = s[0] * inv_d, m0 = a.p.pre == SGB_NORM_LAYER ? s[1] * inv_d : 0.f;
+      team_sum<S>(s, tpr, lds, phase);
+      const float m1 = s[0] * inv_d, m0 = FULL && a.p.pre == SGB_NORM_LAYER ? s[FULL] * inv_d : 0.f;
       get_by(0, qw);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -351,21 +390,21 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = tv[i] * a.p.scale;
       store8(static_cast<R*>(a.dx) + row * a.sdx + col, o, on ? n : 0);
-    float s[2] = {0.f, 0.f};
+    float s[1 + FULL] = {};
     get_by(1, pw);
     if (!GROUPED) get_by(2, gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[i] = (v[i] - mh) * rsh;
         A[i] = fmaf(tv[i], v[i], A[i]);
-        if (BIAS) B[i] += tv[i];
+        if (FULL) B[i] += tv[i];
         tv[i] *= gt[i] * pw[i];  // now b
         s[0] = fmaf(tv[i], v[i], s[0]);
-        s[1] += tv[i];
+        if constexpr (FULL) s[1] += tv[i];
       }
     if (a.p.post != SGB_NORM_NONE) {
-      team_sum(s, tpr, lds, phase);
-      const float m1 = s[0] * inv_d, m0 = a.p.post == SGB_NORM_LAYER ? s[1] * inv_d : 0.f;
+      team_sum<S>(s, tpr, lds, phase);
+      const float m1 = s[0] * inv_d, m0 = FULL && a.p.post == SGB_NORM_LAYER ? s[FULL] * inv_d : 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) tv[i] = (fmaf(-v[i], m1, tv[i]) - m0) * rsh;
     }
@@ -375,13 +414,13 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
       if (on && last_of_gate) {
           float o[8];
           get_by(1, pw);
-          if (BIAS) get_by(3, pb);
+          if (FULL) get_by(3, pb);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             o[i] = A[i] * pw[i];
             P[i] = fmaf(gt[i], A[i], P[i]);
             A[i] = 0.f;
-            if (BIAS) {
+            if (FULL) {
               o[i] = fmaf(B[i], pb[i], o[i]);
               Q[i] = fmaf(gt[i], B[i], Q[i]);
               B[i] = 0.f;
@@ -399,18 +438,18 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   if (!GROUPED) {
     get_by(1, pw);
     get_by(2, gt);
-    if (BIAS) get_by(3, pb);
+    if (FULL) get_by(3, pb);
     if (a.slot && team < a.d.teams) {
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          o[i] = BIAS ? fmaf(B[i], pb[i], A[i] * pw[i]) : A[i] * pw[i];
+          o[i] = FULL ? fmaf(B[i], pb[i], A[i] * pw[i]) : A[i] * pw[i];
         store8(a.slot + team * D + col, o, n);
     }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         P[i] = a.raw ? A[i] : A[i] * gt[i];
-        if (BIAS) Q[i] = a.raw ? B[i] : B[i] * gt[i];
+        if (FULL) Q[i] = a.raw ? B[i] : B[i] * gt[i];
       }
   }
   // the block's teams, added in order
@@ -433,9 +472,9 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
       store8(out + col, s, n);
   };
   put(0, P);
-  if (BIAS) put(1, Q);
+  if (FULL) put(1, Q);
   put(2, C);
-  if (BIAS) put(3, E);
+  if (FULL) put(3, E);
 }
 
 // Adds up what the blocks (or a gate's teams) left, column by column: 16
@@ -467,9 +506,15 @@ __device__ __forceinline__ float join_column(const float* p, int64_t parts, int 
                                              float* lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float s = 0.f;
-  if (col < D) {
-#pragma unroll 8
-    for (int64_t k = wave; k < parts; k += 16) s += p[k * D + col];
+  constexpr int N = 12;  // loads in flight
+  for (int64_t k = wave; k < parts; k += 16 * N) {
+    float v[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      v[u] = load_global<float>(
+          (uintptr_t)(p + min(k + 16 * u, parts - 1) * D + min(col, D - 1)));
+#pragma unroll
+    for (int u = 0; u < N; ++u) s += k + 16 * u < parts ? v[u] : 0.f;
   }
   __syncthreads();
   lds[wave * 64 + lane] = s;
@@ -486,20 +531,28 @@ __global__ __launch_bounds__(1024) void k_norm_join(JoinArgs a) {
   __shared__ float lds[1024];
   const int col = (int)blockIdx.x * 64 + (threadIdx.x & 63);
   const bool mine = threadIdx.x < 64 && col < a.D;
-  if (blockIdx.y >= 2) {  // a gate shared by several teams
-    const int64_t g = blockIdx.y - 2;
+  if (blockIdx.y >= 3) {  // a gate shared by several teams
+    const int64_t g = blockIdx.y - 3;
     const float s = join_column(a.slot + g * a.k * a.D, a.k, a.D, col, lds);
     if (mine) put_as(a.dgate, a.dtype, g * a.sdg + col, s);
     return;
   }
+  if (blockIdx.y > 0) {  // the pre norm's two
+    const int w = 1 + (int)blockIdx.y;
+    if (!a.out[w]) return;
+    const float s = (a.want >> w & 1) ? join_column(a.par + (int64_t)w * a.blocks * a.D, a.blocks,
+                                                    a.D, col, lds)
+                                      : 0.f;
+    if (mine) a.out[w][col] = s;
+    return;
+  }
   float s[2] = {0.f, 0.f};
-  const int w0 = 2 * (int)blockIdx.y;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    if (a.want >> (w0 + i) & 1)
-      s[i] = join_column(a.par + (int64_t)(w0 + i) * a.blocks * a.D, a.blocks, a.D, col, lds);
+    if (a.want >> i & 1)
+      s[i] = join_column(a.par + (int64_t)i * a.blocks * a.D, a.blocks, a.D, col, lds);
   if (!mine) return;
-  if (w0 == 0 && a.raw) {
+  if (a.raw) {
     if (a.dgate) {
       float d = s[0] * (a.post_w ? elem_as(a.post_w, a.pdtype, col) : 1.f);
       if (a.post_b) d = fmaf(s[1], elem_as(a.post_b, a.pdtype, col), d);
@@ -509,8 +562,8 @@ __global__ __launch_bounds__(1024) void k_norm_join(JoinArgs a) {
     s[0] *= gt;
     s[1] *= gt;
   }
-  if (a.out[w0]) a.out[w0][col] = s[0];
-  if (a.out[w0 + 1]) a.out[w0 + 1][col] = s[1];
+  if (a.out[0]) a.out[0][col] = s[0];
+  if (a.out[1]) a.out[1][col] = s[1];
 }
 
 }  // namespace
@@ -578,7 +631,9 @@ template <typename T, typename R>
 void forward_as(const sgb_block_norm_s* p, const FwdArgs& a, unsigned grid, unsigned threads,
                 hipStream_t s) {
   const dim3 g(grid), n(threads);
-  if (p->tpr < 64)
+  if (p->D < 8)
+    hipLaunchKernelGGL((k_norm_forward<T, R, kTiny>), g, n, 0, s, a);
+  else if (p->tpr < 64)
     hipLaunchKernelGGL((k_norm_forward<T, R, kNarrow>), g, n, 0, s, a);
   else if (p->tpr <= 512)
     hipLaunchKernelGGL((k_norm_forward<T, R, kWide>), g, n, 0, s, a);
@@ -587,27 +642,29 @@ void forward_as(const sgb_block_norm_s* p, const FwdArgs& a, unsigned grid, unsi
 }
 
 template <typename T, typename R, int S>
-void backward_shaped(const BwdArgs& a, bool grouped, bool bias, unsigned grid, hipStream_t s) {
+void backward_shaped(const BwdArgs& a, bool grouped, bool full, unsigned grid, hipStream_t s) {
   const dim3 g(grid), n(kThreads<S>);
-  if (grouped && bias)
+  if (grouped && full)
     hipLaunchKernelGGL((k_norm_backward<T, R, S, true, true>), g, n, 0, s, a);
   else if (grouped)
     hipLaunchKernelGGL((k_norm_backward<T, R, S, true, false>), g, n, 0, s, a);
-  else if (bias)
+  else if (full)
     hipLaunchKernelGGL((k_norm_backward<T, R, S, false, true>), g, n, 0, s, a);
   else
     hipLaunchKernelGGL((k_norm_backward<T, R, S, false, false>), g, n, 0, s, a);
 }
 
 template <typename T, typename R>
-void backward_as(const sgb_block_norm_s* p, const BwdArgs& a, bool grouped, bool bias,
+void backward_as(const sgb_block_norm_s* p, const BwdArgs& a, bool grouped, bool full,
                  unsigned grid, hipStream_t s) {
-  if (p->tpr < 64)
-    backward_shaped<T, R, kNarrow>(a, grouped, bias, grid, s);
+  if (p->D < 8)
+    backward_shaped<T, R, kTiny>(a, grouped, full, grid, s);
+  else if (p->tpr < 64)
+    backward_shaped<T, R, kNarrow>(a, grouped, full, grid, s);
   else if (p->tpr <= 512)
-    backward_shaped<T, R, kWide>(a, grouped, bias, grid, s);
+    backward_shaped<T, R, kWide>(a, grouped, full, grid, s);
   else
-    backward_shaped<T, R, kWhole>(a, grouped, bias, grid, s);
+    backward_shaped<T, R, kWhole>(a, grouped, full, grid, s);
 }
 
 #define SGB_LM_NORM_DISPATCH(F, ...)                                         \
@@ -713,7 +770,7 @@ sgb_status sgb_block_norm_forward(sgb_block_norm p, const sgb_norm_params* q,
   a.sxo = f->x_out_stride;
   a.sy = f->y_stride;
   a.rows = R;
-  a.rpg = f->gate ? f->rows_per_gate : R;
+  a.rpg = f->gate ? std::min(f->rows_per_gate, R) : R;
   a.D = D;
   a.tpr = p->tpr;
   // one team a block until every compute unit has one, then fuller blocks
@@ -809,7 +866,7 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
   a.D = D;
   a.tpr = p->tpr;
   a.use_h = use_h;
-  bool grouped = false, bias = false;
+  bool grouped = false, full = false;
   bool parts = false;  // does a gate's sum come from several teams?
   if (R > 0) {
     a.d = deal_rows(p, R, rpg, b->gate != nullptr);
@@ -826,13 +883,13 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
     a.par = reinterpret_cast<float*>(static_cast<char*>(ws) + kHeaderBytes);
     a.slot = parts ? a.par + (int64_t)4 * a.blocks * D : nullptr;
     grouped = !a.d.split && b->gate;
-    bias = (a.want & 10) || gate_bias;
+    full = (a.want & 10) || gate_bias || p->post == SGB_NORM_LAYER || p->pre == SGB_NORM_LAYER;
   }
   DeviceGuard guard(p->device);
   if (!guard.ok) return SGB_ERR_HIP;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream_);
   if (R > 0) {
-    SGB_LM_NORM_DISPATCH(backward_as, p, a, grouped, bias, (unsigned)a.blocks, s);
+    SGB_LM_NORM_DISPATCH(backward_as, p, a, grouped, full, (unsigned)a.blocks, s);
   }
   if (a.want || parts ||
       (R == 0 && (b->d_post_weight || b->d_post_bias || b->d_pre_weight || b->d_pre_bias))) {
@@ -855,7 +912,7 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
     j.raw = a.raw;
     j.pdtype = q->dtype;
     j.dtype = dtype;
-    const unsigned ys = 2 + (parts ? (unsigned)a.d.groups : 0u);
+    const unsigned ys = 3 + (parts ? (unsigned)a.d.groups : 0u);
     hipLaunchKernelGGL(k_norm_join, dim3((unsigned)div_up(D, 64), ys), dim3(1024), 0, s, j);
   }
   return hipGetLastError() == hipSuccess ? SGB_OK : SGB_ERR_HIP;

@@ -104,10 +104,13 @@ __global__ __launch_bounds__(kMostThreads) void k_penalty(Args a) {
     bias_id[u] = load_global<int32_t>(
         a.biases ? (uintptr_t)(bias_ids + min(t + u * nt, a.biases - 1)) : (uintptr_t)kNowhere);
   const T* x = static_cast<const T*>(a.logits) + row * a.sl;
+  // a last slice of fewer than eight has the elements before it loaded too
+  const T* from = x + max(v0 - 8, (int64_t)0);
+  const uint32_t off = v0 > 0 ? 8 : 0;
   Raw8<T> raw[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k)
-    raw[k] = ask8(x, v0 + (k * nt + t) * 8, max(v0 + size, min(a.V, (int64_t)8)));
+    raw[k] = ask8(a.V < 8 ? nullptr : from, off + (k * nt + t) * 8, off + size);
   for (int i = t * 4; i < a.slice; i += nt * 4)
     *reinterpret_cast<uint4*>(word + i) = make_uint4(0, 0, 0, 0);
   if (t == 0) twice = 0;
@@ -170,7 +173,10 @@ __global__ __launch_bounds__(kMostThreads) void k_penalty(Args a) {
     const int i = (k * nt + t) * 8;
     if (i >= size) break;
     const uint32_t ok = allowed ? allowed[i >> 3] : 0xffu;
-    have8(raw[k], x, v0 + i, a.V, size - i);
+    if (k == 0 && a.V < 8)
+      raw[k] = load8(x + i, size - i);
+    else
+      have8(raw[k], size - i);
     float v[8];
     widen8(raw[k], v);
     const uint4 w0 = *reinterpret_cast<const uint4*>(word + i);
