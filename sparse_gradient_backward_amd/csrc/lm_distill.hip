@@ -27,6 +27,9 @@ constexpr int kThreads = 256;
 constexpr int kStep = kThreads * 8;    // columns a workgroup takes at a time
 constexpr int kMaxSpan = 131072;       // columns a workgroup takes in all (16 KB of bits)
 constexpr int kMaxSplit = 64;          // workgroups a row
+#ifndef SGB_ROWMIN
+#define SGB_ROWMIN 1
+#endif
 constexpr int kMaxK = 1024;
 constexpr int64_t kMaxV = (int64_t)kMaxSpan * kMaxSplit;
 
@@ -216,30 +219,42 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// What a row's terms need beside the sums over its logits (one wave): nothing
+// here waits for them.
+struct Known {
+  double entropy;   // sum of p log p
+  double reach;     // sum of p (x - top)
+  double psum;      // sum of p
+  double ls, ls1;   // sums of exp((x - top) / T), of exp(x - top), an id once
+  float top;        // the largest listed logit
+  float label_x, w, above;
+  int64_t label;    // -1: none
+  int some, repeated;
+};
+
 template <typename T, bool TAIL, bool TWO>
-__device__ void row_terms(const Args& a, int64_t row, float4 sums, Listed l, Terms& o,
-                          double& loss) {
+__device__ __forceinline__ void gather(const Args& a, int64_t row, const Listed& l, Known& o) {
   const int lane = threadIdx.x & 63;
   const T* logits = static_cast<const T*>(a.logits) + row * a.sl;
   const double invT = 1.0 / (double)a.T;
-  const float w = weight_of(a, row);
-  o.above = w * a.scale * (a.grad_loss ? a.grad_loss[row] : 1.f);
-  o.m = sums.x;
+  o.w = weight_of(a, row);
+  o.above = o.w * a.scale * (a.grad_loss ? a.grad_loss[row] : 1.f);
 
   for (int i = lane; i < a.table; i += 64) l.table[i] = -1;
   wave_sync();
-  bool bad = false, twice = false;
-  float tmax = -FLT_MAX;
-  bool some = false;
+  bool bad = false, twice = false, some = false;
+  float tmax = -FLT_MAX, top = -FLT_MAX;
   for (int k = lane; k < a.K; k += 64) {
     const int64_t id64 = a.ids[row * a.si + k];
     const bool there = id64 >= 0 && id64 < a.V;
     bad |= id64 >= a.V;
     const int32_t id = there ? (int32_t)id64 : -1;
+    const float x = there ? widen(logits[id]) : 0.f;
     int own = 0;
     if (there) {
       some = true;
       tmax = fmaxf(tmax, a.values[row * a.sv + k]);
+      top = fmaxf(top, x);
       uint32_t at = (uint32_t)id * 2654435761u >> 7;
       while (true) {  // at most K of the table's >= 2 K places are taken
         at &= (uint32_t)a.table - 1;
@@ -252,11 +267,12 @@ __device__ void row_terms(const Args& a, int64_t row, float4 sums, Listed l, Ter
     }
     l.id[k] = id;
     l.owner[k] = own;
-    l.x[k] = there ? widen(logits[id]) : 0.f;
+    l.x[k] = x;
   }
-  some = __ballot(some) != 0;
+  o.some = __ballot(some) != 0;
   o.repeated = __ballot(twice) != 0;
   tmax = wave_max(tmax);
+  o.top = wave_max(top);
 
   // the teacher's log-sum-exp
   double tl;
@@ -269,65 +285,81 @@ __device__ void row_terms(const Args& a, int64_t row, float4 sums, Listed l, Ter
     z = wave_add(z);
     tl = z == 0.0 ? HUGE_VAL : (double)tmax * invT + log(z);  // nothing: every p is 0
   }
-
-  // the student's, the listed ones added to what the pass left out
-  double m = (double)sums.x, s = (double)sums.y, s1 = (double)sums.z;
-  const double log_out = log(s);
-  if (TAIL) {
-    float lm = -FLT_MAX;
-    for (int k = lane; k < a.K; k += 64)
-      if (l.owner[k]) lm = fmaxf(lm, l.x[k]);
-    lm = wave_max(lm);
-    const double mm = fmax(m, (double)lm);
-    double ls = 0.0, ls1 = 0.0;
-    for (int k = lane; k < a.K; k += 64)
-      if (l.owner[k]) {
-        const double d = (double)l.x[k] - mm;
-        ls += exp(d * invT);
-        if (TWO) ls1 += exp(d);
-      }
-    s = s * exp((m - mm) * invT) + wave_add(ls);
-    if (TWO) s1 = s1 * exp(m - mm) + wave_add(ls1);
-    m = mm;
-  }
-  o.base = m;
-  o.lse_out = ((double)sums.x - m) * invT + log_out;
-  o.lse = log(s);
-  o.lse1 = TWO ? log(s1) : o.lse;  // without a second sum T is 1 or there is no label
-
-  double kl = 0.0, psum = 0.0;
+  double entropy = 0.0, reach = 0.0, psum = 0.0, ls = 0.0, ls1 = 0.0;
   for (int k = lane; k < a.K; k += 64) {
     double p = 0.0;
+    const double d = (double)l.x[k] - (double)o.top;
     if (l.id[k] >= 0) {
       const double lp = (double)a.values[row * a.sv + k] * invT - tl;
       p = lp < -800.0 ? 0.0 : exp(lp);
-      if (!(p <= 0.0)) kl += p * (lp - (((double)l.x[k] - m) * invT - o.lse));
+      if (!(p <= 0.0)) {
+        entropy += p * lp;
+        reach += p * d;
+      }
     }
     psum += p;
     l.p[k] = (float)p;
+    if (TAIL && l.owner[k]) {
+      ls += exp(d * invT);
+      if (TWO) ls1 += exp(d);
+    }
   }
-  psum = wave_add(psum);
-  kl = wave_add(kl);
-  o.tail = 0.0;
-  o.mass = psum == 0.0 ? 0.0 : 1.0;
-  if (TAIL) {
-    o.tail = some ? fmax(0.0, 1.0 - psum) : 0.0;
-    o.mass = psum + o.tail;
-    if (o.tail > 0.0) kl += o.tail * (log(o.tail) - (o.lse_out - o.lse));
-  }
-  loss = (double)a.kd * (double)a.T * (double)a.T * kl;
+  o.entropy = wave_add(entropy);
+  o.reach = wave_add(reach);
+  o.psum = wave_add(psum);
+  o.ls = TAIL ? wave_add(ls) : 0.0;
+  o.ls1 = TAIL && TWO ? wave_add(ls1) : 0.0;
 
   o.label = -1;
+  o.label_x = 0.f;
   if (a.labels) {
     const int64_t lab = a.labels[row];
     bad |= lab >= a.V;
     if (lab >= 0 && lab < a.V) {
       o.label = lab;
-      loss += (double)a.ce * (o.lse1 - ((double)widen(logits[lab]) - m));
+      o.label_x = widen(logits[lab]);
     }
   }
-  loss *= (double)w;
   if (__ballot(bad) && lane == 0) set_status(a.hdr, a.epoch, SGB_ERR_INDEX_OUT_OF_RANGE);
+  wave_sync();
+}
+
+// The row's terms and loss from the sums over its logits (with a tail: over
+// those not listed).
+template <bool TAIL, bool TWO>
+__device__ __forceinline__ void finish(const Args& a, const Known& n, float4 sums, Terms& o,
+                                       double& loss) {
+  const double invT = 1.0 / (double)a.T;
+  double m = (double)sums.x, s = (double)sums.y, s1 = (double)sums.z;
+  const double log_out = TAIL ? log(s) : 0.0;
+  if (TAIL) {
+    const double mm = fmax(m, (double)n.top), from = m - mm, listed = (double)n.top - mm;
+    s = s * exp(from * invT) + n.ls * exp(listed * invT);
+    if (TWO) s1 = s1 * exp(from) + n.ls1 * exp(listed);
+    m = mm;
+  }
+  o.m = sums.x;
+  o.above = n.above;
+  o.repeated = n.repeated;
+  o.label = n.label;
+  o.base = m;
+  o.lse = log(s);
+  o.lse_out = TAIL ? ((double)sums.x - m) * invT + log_out : o.lse;
+  o.lse1 = TWO ? log(s1) : o.lse;  // without a second sum T is 1 or there is no label
+
+  double kl = 0.0;
+  if (n.psum != 0.0)
+    kl = n.entropy - (n.reach + ((double)n.top - m) * n.psum) * invT + o.lse * n.psum;
+  o.tail = 0.0;
+  o.mass = n.psum == 0.0 ? 0.0 : 1.0;
+  if (TAIL) {
+    o.tail = n.some ? fmax(0.0, 1.0 - n.psum) : 0.0;
+    o.mass = n.psum + o.tail;
+    if (o.tail > 0.0) kl += o.tail * (log(o.tail) - (o.lse_out - o.lse));
+  }
+  loss = (double)a.kd * (double)a.T * (double)a.T * kl;
+  if (n.label >= 0) loss += (double)a.ce * (o.lse1 - ((double)n.label_x - m));
+  loss *= (double)n.w;
 
   // ca, cb: relative to the pass's own maximum and sum
   const double kt = (double)o.above * (double)a.kd * (double)a.T;
@@ -346,7 +378,14 @@ __device__ void row_terms(const Args& a, int64_t row, float4 sums, Listed l, Ter
   }
   o.ca = (float)ca;
   o.cb = (float)cb;
-  wave_sync();
+}
+
+template <typename T, bool TAIL, bool TWO>
+__device__ void row_terms(const Args& a, int64_t row, float4 sums, Listed l, Terms& o,
+                          double& loss) {
+  Known n;
+  gather<T, TAIL, TWO>(a, row, l, n);
+  finish<TAIL, TWO>(a, n, sums, o, loss);
 }
 
 // The row's partial sums joined (one wave).
@@ -479,6 +518,186 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(Args a) {
   if (threadIdx.x < 64) patch<T, TAIL>(a, row, c0, c1, t, l);
 }
 
+// ------------------------------------------------------------- a row at once
+//
+// Loss and gradient of rows that a workgroup's registers can hold (up to 128
+// logits of 16 bits a lane, 64 of 32): read once, their maximum, the sums
+// relative to it, the terms, and the gradient from the same registers.  The
+// workgroup stays for several rows: as a part of the gradient is stored, the
+// next row's logits are asked for in its place, and the last wave gathers the
+// next row's listed terms meanwhile.
+
+// The listed ids of a row in the bits (one wave); `on` false takes them out.
+__device__ __forceinline__ void mark_wave(const Args& a, const Listed& l, uint32_t* bits, bool on) {
+  for (int k = threadIdx.x & 63; k < a.K; k += 64) {
+    const int id = l.id[k];
+    if (id < 0) continue;
+    if (on)
+      atomicOr(&bits[id >> 5], 1u << (id & 31));
+    else
+      bits[id >> 5] = 0;
+  }
+}
+
+template <int NT, typename F>
+__device__ __forceinline__ float block_fold(float x, float* red, F f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  x = wave_fold(x, 64, f);
+  if (lane == 0) red[wave] = x;
+  __syncthreads();
+  x = red[lane % (NT / 64)];
+  return wave_fold(x, NT / 64 < 8 ? 8 : NT / 64, f);
+}
+
+template <typename T, bool TAIL, bool TWO, int NT, int NC>
+__global__ __launch_bounds__(NT) void k_distill_row(Args a) {
+  extern __shared__ char lds[];
+  __shared__ Terms terms;
+  __shared__ Known known[2];
+  __shared__ float red[3][NT / 64];
+  const int t = (int)threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  constexpr int kLast = NT / 64 - 1;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(lds);  // TAIL: a bit a logit
+  char* lists = lds + (TAIL ? a.span / 8 : 0);
+  const int list_bytes = (int)listed_bytes(a.K, a.table);
+  if (blockIdx.x == 0 && t == 0) a.hdr->epoch = a.epoch;
+  const uint32_t V = (uint32_t)a.V;
+
+  // the next row at or after `row` that counts; padding rows are written on the way
+  auto settle = [&](int64_t row) {
+    while (row < a.rows && weight_of(a, row) == 0.f) {
+      T* grad = static_cast<T*>(a.grad) + row * a.sg;
+      const float zero[8] = {};
+      for (uint32_t col = t * 8; col < V; col += NT * 8) store8(grad + col, zero, (int)min(8u, V - col));
+      if (t == 0) a.loss[row] = 0.f;
+      row += gridDim.x;
+    }
+    return row;
+  };
+
+  int64_t row = settle(blockIdx.x);
+  if (row >= a.rows) return;
+  Raw8<T> raw[NC];
+  const T* x = static_cast<const T*>(a.logits) + row * a.sl;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) raw[c] = ask8(x, (c * NT + t) * 8, V);
+  if (TAIL) {
+    for (int i = t; i < a.span / 32; i += NT) bits[i] = 0;
+    __syncthreads();
+  }
+  int par = 0;
+  if (wave == kLast) {
+    const Listed l = listed_in(lists, a.K);
+    Known n;
+    gather<T, TAIL, TWO>(a, row, l, n);
+    if (TAIL) mark_wave(a, l, bits, true);
+    if ((t & 63) == 0) known[0] = n;
+  }
+  __syncthreads();
+
+  while (true) {
+    // the largest, with what is left out set to -inf
+    float top = -FLT_MAX;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * NT + t) * 8, n = (int)V - col;
+      if (n < 8) have8(raw[c], n);
+      uint32_t skip = n < 8 ? (n > 0 ? 0xffu << n : 0xffu) & 0xffu : 0u;
+      if (TAIL && n > 0) skip |= reinterpret_cast<const uint8_t*>(bits)[col >> 3];
+      if (skip) {
+        constexpr int W = Vec<T>::kWords;
+        constexpr uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : __is_same(T, bf16_t) ? 0xff80u : 0xfc00u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (W == 8) {
+            raw[c].w[i] = skip >> i & 1 ? ninf : raw[c].w[i];
+          } else {
+            const uint32_t keep = i & 1 ? 0xffffu : 0xffff0000u;
+            const uint32_t w = (raw[c].w[i >> 1] & keep) | (ninf << (16 * (i & 1)));
+            raw[c].w[i >> 1] = skip >> i & 1 ? w : raw[c].w[i >> 1];
+          }
+        }
+      }
+      float v[8];
+      widen8(raw[c], v);
+      top = fmaxf(fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])),
+                        fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7]))), top);
+    }
+    top = block_fold<NT>(top, red[0], [](float p, float q) { return fmaxf(p, q); });
+    float s = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float v[8], p[8];
+      widen8(raw[c], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = exp2_of((v[i] - top) * a.c);
+      s += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      if (TWO) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = exp2_of((v[i] - top) * kLog2e);
+        s1 += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      }
+    }
+    auto add = [](float p, float q) { return p + q; };
+    const int lane = t & 63;
+    s = wave_fold(s, 64, add);
+    if (TWO) s1 = wave_fold(s1, 64, add);
+    if (lane == 0) {
+      red[1][wave] = s;
+      red[2][wave] = s1;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      s = s1 = 0.f;
+      for (int w = 0; w < NT / 64; ++w) s += red[1][w], s1 += red[2][w];
+      Terms mine;
+      double loss;
+      finish<TAIL, TWO>(a, known[par], make_float4(top, s, s1, 0.f), mine, loss);
+      if (t == 0) {
+        terms = mine;
+        a.loss[row] = (float)loss;
+      }
+    }
+    __syncthreads();
+
+    const int64_t next = settle(row + gridDim.x);
+    const bool more = next < a.rows;
+    if (more && wave == kLast) {
+      const Listed l = listed_in(lists + (par ^ 1) * list_bytes, a.K);
+      if (TAIL) mark_wave(a, listed_in(lists + par * list_bytes, a.K), bits, false);
+      Known n;
+      gather<T, TAIL, TWO>(a, next, l, n);
+      if (TAIL) mark_wave(a, l, bits, true);
+      if (lane == 0) known[par ^ 1] = n;
+    }
+    const float m = terms.m, ca = terms.ca, cb = terms.cb;
+    T* grad = static_cast<T*>(a.grad) + row * a.sg;
+    x = static_cast<const T*>(a.logits) + next * a.sl;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * NT + t) * 8;
+      float v[8];
+      widen8(raw[c], v);
+      if (more) raw[c] = ask8(x, col, V);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = v[i] - m;
+        float g = ca * exp2_of(d * a.c);
+        if (TWO) g = fmaf(cb, exp2_of(d * kLog2e), g);
+        v[i] = g;
+      }
+      store8(grad + col, v, (int)V - col);
+    }
+    __syncthreads();  // the stream's stores come before the patch's
+    if (wave == 0)
+      patch<T, TAIL>(a, row, 0, a.V, terms, listed_in(lists + par * list_bytes, a.K));
+    if (!more) return;
+    row = next;
+    par ^= 1;
+  }
+}
+
 }  // namespace
 
 // ------------------------------------------------------------- host
@@ -503,8 +722,36 @@ int split_of(const sgb_distill_s* p, int64_t rows) {
 
 enum What { kLoss, kBackward, kBoth };
 
+template <typename T, bool TAIL, bool TWO, int NT, int NC>
+void run_rows(Args a, int cus, hipStream_t s) {
+  a.span = (int)align_up((size_t)a.V, 32);
+  const int64_t grid = std::min(a.rows, (int64_t)cus * (1024 / NT));
+  const size_t lds = (TAIL ? a.span / 8 : 0) + 2 * listed_bytes(a.K, a.table);
+  hipLaunchKernelGGL((k_distill_row<T, TAIL, TWO, NT, NC>), dim3((unsigned)grid), dim3(NT), lds, s, a);
+}
+
+// Does a row of V logits of T fit in a workgroup's registers, and are there
+// rows enough to fill the card a workgroup a row?
+template <typename T>
+bool at_once(const Args& a, int cus) {
+  return a.V >= 8 && a.V <= (sizeof(T) == 4 ? 65536 : 131072) && a.K <= 512 && a.rows >= SGB_ROWMIN;
+}
+
 template <typename T, bool TAIL, bool TWO>
-void run_as(const Args& a, What what, hipStream_t s) {
+void run_as(const Args& a, What what, int cus, hipStream_t s) {
+  if (what == kBoth && at_once<T>(a, cus)) {
+    if (a.V <= 8192)
+      run_rows<T, TAIL, TWO, 256, 4>(a, cus, s);
+    else if (a.V <= 16384)
+      run_rows<T, TAIL, TWO, 256, 8>(a, cus, s);
+    else if (a.V <= 32768)
+      run_rows<T, TAIL, TWO, 512, 8>(a, cus, s);
+    else if (a.V <= 65536)
+      run_rows<T, TAIL, TWO, 1024, 8>(a, cus, s);
+    else if constexpr (sizeof(T) == 2)
+      run_rows<T, TAIL, TWO, 1024, 16>(a, cus, s);
+    return;
+  }
   const dim3 grid((unsigned)(a.rows * a.split));
   const size_t terms = listed_bytes(a.K, a.table);
   if (what != kBackward)
@@ -518,16 +765,16 @@ void run_as(const Args& a, What what, hipStream_t s) {
 }
 
 template <typename T>
-void run_typed(const Args& a, What what, hipStream_t s) {
+void run_typed(const Args& a, What what, int cus, hipStream_t s) {
   const bool tail = a.teacher_lse != nullptr, two = a.labels && a.T != 1.f;
   if (tail && two)
-    run_as<T, true, true>(a, what, s);
+    run_as<T, true, true>(a, what, cus, s);
   else if (tail)
-    run_as<T, true, false>(a, what, s);
+    run_as<T, true, false>(a, what, cus, s);
   else if (two)
-    run_as<T, false, true>(a, what, s);
+    run_as<T, false, true>(a, what, cus, s);
   else
-    run_as<T, false, false>(a, what, s);
+    run_as<T, false, false>(a, what, cus, s);
 }
 
 sgb_status run(sgb_distill p, const sgb_distill_args* q, void* ws, size_t ws_bytes, void* stream_,
@@ -593,11 +840,11 @@ sgb_status run(sgb_distill p, const sgb_distill_args* q, void* ws, size_t ws_byt
   a.scale = what == kLoss ? 1.f : q->grad_scale;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream_);
   if (q->dtype == SGB_F32)
-    run_typed<float>(a, what, s);
+    run_typed<float>(a, what, p->cus, s);
   else if (q->dtype == SGB_BF16)
-    run_typed<bf16_t>(a, what, s);
+    run_typed<bf16_t>(a, what, p->cus, s);
   else
-    run_typed<f16_t>(a, what, s);
+    run_typed<f16_t>(a, what, p->cus, s);
   return hipGetLastError() == hipSuccess ? SGB_OK : SGB_ERR_HIP;
 }
 

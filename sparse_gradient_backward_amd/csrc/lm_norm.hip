@@ -581,13 +581,13 @@ namespace {
 
 int max_threads(const sgb_block_norm_s* p) { return p->tpr > 512 ? kThreads<kWhole> : kThreads<kWide>; }
 
-// Blocks of the backward: one or two fill a compute unit's registers.
-int64_t backward_blocks(const sgb_block_norm_s* p) {
-  return (int64_t)p->cus * (p->tpr > 512 ? 1 : 2);
+// Most blocks of the backward: one or two fill a compute unit's registers.
+int64_t backward_blocks(const sgb_block_norm_s* p, bool light) {
+  return (int64_t)p->cus * (p->tpr > 512 || !light ? 1 : 2);
 }
 
-Deal deal_rows(const sgb_block_norm_s* p, int64_t rows, int64_t rpg, bool gate) {
-  const int64_t target = backward_blocks(p) * (max_threads(p) / p->tpr);
+Deal deal_rows(const sgb_block_norm_s* p, int64_t rows, int64_t rpg, bool gate, bool light) {
+  const int64_t target = backward_blocks(p, light) * (max_threads(p) / p->tpr);
   const int64_t rp = std::max<int64_t>(1, div_up(rows, target));
   Deal d{};
   d.groups = div_up(rows, rpg);
@@ -719,7 +719,7 @@ sgb_status sgb_block_norm_workspace_bytes(sgb_block_norm p, int64_t rows, size_t
   // each has at most target / (n - 1) + 1 teams (the last gate may have few
   // rows): the most, 2 target + 2, is with two; with rp = 1, 2 rows.
   const int64_t per_block = max_threads(p) / p->tpr;
-  const int64_t target = backward_blocks(p) * per_block;
+  const int64_t target = backward_blocks(p, true) * per_block;
   const int64_t teams = std::min(2 * std::max<int64_t>(rows, 1), 2 * target + 2);
   const int64_t blocks = div_up(teams, per_block);
   *bytes = kHeaderBytes + align_up((size_t)(4 * blocks + teams) * p->D * sizeof(float), 256);
@@ -869,11 +869,17 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
   bool grouped = false, full = false;
   bool parts = false;  // does a gate's sum come from several teams?
   if (R > 0) {
-    a.d = deal_rows(p, R, rpg, b->gate != nullptr);
+    const bool gate_bias = q->post_bias && b->d_gate;
+    full = b->d_post_bias || b->d_pre_bias || gate_bias || p->post == SGB_NORM_LAYER ||
+           p->pre == SGB_NORM_LAYER;
+    // Two workgroups share a compute unit only where a lane's values fit in 128
+    // registers; else a second would wait for the first to end.
+    a.d = deal_rows(p, R, rpg, b->gate != nullptr, true);
+    if (full || er == 4 || (b->gate && !a.d.split))
+      a.d = deal_rows(p, R, rpg, b->gate != nullptr, false);
     const int64_t per_block = max_threads(p) / p->tpr;
     a.blocks = (int)div_up(a.d.teams, per_block);
     a.raw = a.d.split && a.d.groups == 1;
-    const bool gate_bias = q->post_bias && b->d_gate;
     a.want = ((b->d_post_weight || (a.raw && b->d_gate)) ? 1 : 0) |
              ((b->d_post_bias || (a.raw && gate_bias)) ? 2 : 0) | (b->d_pre_weight ? 4 : 0) |
              (b->d_pre_bias ? 8 : 0);
@@ -883,7 +889,6 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
     a.par = reinterpret_cast<float*>(static_cast<char*>(ws) + kHeaderBytes);
     a.slot = parts ? a.par + (int64_t)4 * a.blocks * D : nullptr;
     grouped = !a.d.split && b->gate;
-    full = (a.want & 10) || gate_bias || p->post == SGB_NORM_LAYER || p->pre == SGB_NORM_LAYER;
   }
   DeviceGuard guard(p->device);
   if (!guard.ok) return SGB_ERR_HIP;
