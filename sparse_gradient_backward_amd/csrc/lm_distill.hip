@@ -549,8 +549,16 @@ __device__ __forceinline__ float block_fold(float x, float* red, F f) {
   return wave_fold(x, NT / 64 < 8 ? 8 : NT / 64, f);
 }
 
+// Keeps the compiler from holding what it made of the registers in one pass
+// (the same logits in fp32, twice their size) for the next.
+template <typename T>
+__device__ __forceinline__ void forget(Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < Vec<T>::kWords; ++i) asm volatile("" : "+v"(r.w[i]));
+}
+
 template <typename T, bool TAIL, bool TWO, int NT, int NC>
-__global__ __launch_bounds__(NT) void k_distill_row(Args a) {
+__global__ __launch_bounds__(NT, 2) void k_distill_row(Args a) {
   extern __shared__ char lds[];
   __shared__ Terms terms;
   __shared__ Known known[2];
@@ -599,9 +607,11 @@ __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
   while (true) {
     // the largest, with what is left out set to -inf
     float top = -FLT_MAX;
+    int at = t * 8;
+    asm volatile("" : "+v"(at));  // not kept in registers for every part
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * NT + t) * 8, n = (int)V - col;
+      const int col = c * NT * 8 + at, n = (int)V - col;
       if (n < 8) have8(raw[c], n);
       uint32_t skip = n < 8 ? (n > 0 ? 0xffu << n : 0xffu) & 0xffu : 0u;
       if (TAIL && n > 0) skip |= reinterpret_cast<const uint8_t*>(bits)[col >> 3];
@@ -629,6 +639,7 @@ __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float v[8], p[8];
+      forget(raw[c]);
       widen8(raw[c], v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = exp2_of((v[i] - top) * a.c);
@@ -674,10 +685,13 @@ __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
     const float m = terms.m, ca = terms.ca, cb = terms.cb;
     T* grad = static_cast<T*>(a.grad) + row * a.sg;
     x = static_cast<const T*>(a.logits) + next * a.sl;
+    at = t * 8;
+    asm volatile("" : "+v"(at));
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = (c * NT + t) * 8;
+      const int col = c * NT * 8 + at;
       float v[8];
+      forget(raw[c]);
       widen8(raw[c], v);
       if (more) raw[c] = ask8(x, col, V);
 #pragma unroll
@@ -687,7 +701,7 @@ __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
         if (TWO) g = fmaf(cb, exp2_of(d * kLog2e), g);
         v[i] = g;
       }
-      store8(grad + col, v, (int)V - col);
+      store8(grad, (uint32_t)col, v, (int)V - col);
     }
     __syncthreads();  // the stream's stores come before the patch's
     if (wave == 0)
@@ -725,7 +739,7 @@ enum What { kLoss, kBackward, kBoth };
 template <typename T, bool TAIL, bool TWO, int NT, int NC>
 void run_rows(Args a, int cus, hipStream_t s) {
   a.span = (int)align_up((size_t)a.V, 32);
-  const int64_t grid = std::min(a.rows, (int64_t)cus * (1024 / NT));
+  const int64_t grid = std::min(a.rows, (int64_t)cus * (NT == 512 ? 1 : NC * sizeof(T) >= 64 ? 2 : 3));
   const size_t lds = (TAIL ? a.span / 8 : 0) + 2 * listed_bytes(a.K, a.table);
   hipLaunchKernelGGL((k_distill_row<T, TAIL, TWO, NT, NC>), dim3((unsigned)grid), dim3(NT), lds, s, a);
 }
@@ -745,11 +759,13 @@ void run_as(const Args& a, What what, int cus, hipStream_t s) {
     else if (a.V <= 16384)
       run_rows<T, TAIL, TWO, 256, 8>(a, cus, s);
     else if (a.V <= 32768)
-      run_rows<T, TAIL, TWO, 512, 8>(a, cus, s);
+      run_rows<T, TAIL, TWO, 256, 16>(a, cus, s);
+    else if constexpr (sizeof(T) == 4)
+      run_rows<T, TAIL, TWO, 512, 16>(a, cus, s);
     else if (a.V <= 65536)
-      run_rows<T, TAIL, TWO, 1024, 8>(a, cus, s);
-    else if constexpr (sizeof(T) == 2)
-      run_rows<T, TAIL, TWO, 1024, 16>(a, cus, s);
+      run_rows<T, TAIL, TWO, 256, 32>(a, cus, s);
+    else
+      run_rows<T, TAIL, TWO, 512, 32>(a, cus, s);
     return;
   }
   const dim3 grid((unsigned)(a.rows * a.split));

@@ -151,8 +151,18 @@ __device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
 // out what is still to be read (block norms of 8192 x 4096: 82 -> 72 us;
 // penalties on 512 x 131072 fp32: 105 -> 101; sums of 4096 x 131072 logits whose
 // gradient was written before: 214 -> 178).
+template <typename U, typename V>
+__device__ __forceinline__ void store_global(void* p, uint32_t bytes, V v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __builtin_nontemporal_store(
+      v, reinterpret_cast<__attribute__((address_space(1))) U*>(
+             reinterpret_cast<__attribute__((address_space(1))) char*>((uintptr_t)p) + bytes));
+#endif
+}
+
+// (`row` is best uniform and `at` the lane's, as for loads.)
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
+__device__ __forceinline__ void store8(T* row, uint32_t at, const float (&v)[8], int n) {
   typename Vec<T>::type t;
 #pragma unroll
   for (int i = 0; i < 8; ++i) t[i] = (T)v[i];
@@ -165,12 +175,17 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
     };
     const Quads r = __builtin_bit_cast(Quads, t);
 #pragma unroll
-    for (int i = 0; i < W; ++i) __builtin_nontemporal_store(r.q[i], reinterpret_cast<Any*>(p) + i);
+    for (int i = 0; i < W; ++i) store_global<Any>(row, at * (uint32_t)sizeof(T) + 16 * i, r.q[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
-      if (i < n) p[i] = t[i];
+      if (i < n) row[at + i] = t[i];
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
+  store8(p, 0u, v, n);
 }
 
 // Eight elements of a type known at run time.

@@ -193,14 +193,14 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_forward(FwdArgs a) {
         xo[i] = fmaf(a.p.scale, xo[i], g[i] * z);
       }
     const bool on = row < a.rows;
-      store8(static_cast<R*>(a.x_out) + row * a.sxo + col, xo, on ? n : 0);
+      store8(static_cast<R*>(a.x_out) + row * a.sxo, (uint32_t)col, xo, on ? n : 0);
     row_stats<S>(xo, n, a.p.pre, inv_d, a.p.pre_eps, tpr, lds, phase, mx, rsx);
     if (a.y) {
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           y[i] = fmaf((xo[i] - mx) * rsx, qw[i], qb[i]);
-        store8(static_cast<T*>(a.y) + row * a.sy + col, y, on ? n : 0);
+        store8(static_cast<T*>(a.y) + row * a.sy, (uint32_t)col, y, on ? n : 0);
     }
     if (a.stats && on && t == 0) {
       float* s = a.stats + row * 4;
@@ -389,7 +389,7 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
     float o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = tv[i] * a.p.scale;
-      store8(static_cast<R*>(a.dx) + row * a.sdx + col, o, on ? n : 0);
+      store8(static_cast<R*>(a.dx) + row * a.sdx, (uint32_t)col, o, on ? n : 0);
     float s[1 + FULL] = {};
     get_by(1, pw);
     if (!GROUPED) get_by(2, gt);
@@ -408,7 +408,7 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) tv[i] = (fmaf(-v[i], m1, tv[i]) - m0) * rsh;
     }
-      store8(static_cast<T*>(a.dh) + row * a.sdh + col, tv, on ? n : 0);
+      store8(static_cast<T*>(a.dh) + row * a.sdh, (uint32_t)col, tv, on ? n : 0);
 
     if (GROUPED) {
       if (on && last_of_gate) {
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
               B[i] = 0.f;
             }
           }
-          if (a.dgate) store8(static_cast<T*>(a.dgate) + g * a.sdg + col, o, n);
+          if (a.dgate) store8(static_cast<T*>(a.dgate) + g * a.sdg, (uint32_t)col, o, n);
       }
       if (--left == 0) {
         left = a.rpg;
