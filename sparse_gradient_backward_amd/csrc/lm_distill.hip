@@ -27,9 +27,7 @@ constexpr int kThreads = 256;
 constexpr int kStep = kThreads * 8;    // columns a workgroup takes at a time
 constexpr int kMaxSpan = 131072;       // columns a workgroup takes in all (16 KB of bits)
 constexpr int kMaxSplit = 64;          // workgroups a row
-#ifndef SGB_ROWMIN
-#define SGB_ROWMIN 1
-#endif
+constexpr size_t kShortRow = 32768;    // bytes
 constexpr int kMaxK = 1024;
 constexpr int64_t kMaxV = (int64_t)kMaxSpan * kMaxSplit;
 
@@ -99,55 +97,73 @@ struct Sums {
   }
 };
 
-// ------------------------------------------------------------- sums of a row
+// ------------------------------------------------------------- streams
+
+// f(eight logits as loaded, column) over columns [c0, c1) of a row, kAhead
+// loads of a lane in flight.  Every lane makes every turn; f looks at the column.
+constexpr int kAhead = 2;
+
+template <int NT, typename T, typename F>
+__device__ __forceinline__ void stream(const T* row, uint32_t c0, uint32_t c1, uint32_t V, F f) {
+  constexpr uint32_t kStride = NT * 8;
+  uint32_t col = c0 + threadIdx.x * 8;
+  if (V < 8) {  // a load of eight does not fit
+    const int n = (int)V - (int)col;
+    f(load8(row + col, n), col, n);
+    return;
+  }
+  Raw8<T> q[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) q[u] = ask8(row, col + u * kStride, c1);
+  for (uint32_t base = c0; base < c1; base += kAhead * kStride) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      Raw8<T> r = q[u];
+      q[u] = ask8(row, col + kAhead * kStride, c1);
+      const int n = (int)c1 - (int)col;
+      have8(r, n);
+      f(r, col, n);
+      col += kStride;
+    }
+  }
+}
+
+template <int NT, typename T>
+__device__ __forceinline__ void write_zeros(T* grad, uint32_t c0, uint32_t c1) {
+  const float zero[8] = {};
+  for (uint32_t col = c0 + threadIdx.x * 8; col < c1; col += NT * 8)
+    store8(grad, col, zero, (int)(c1 - col));
+}
 
 // Sets the bits of the row's listed ids in columns [c0, c1).
+template <int NT>
 __device__ __forceinline__ void mark_listed(const Args& a, int64_t row, int64_t c0, int64_t c1,
                                             uint32_t* bits) {
-  for (int k = threadIdx.x; k < a.K; k += kThreads) {
+  for (int k = threadIdx.x; k < a.K; k += NT) {
     const int64_t id = a.ids[row * a.si + k];
     if (id >= c0 && id < c1) atomicOr(&bits[(id - c0) >> 5], 1u << ((id - c0) & 31));
   }
 }
 
-template <typename T, bool TAIL, bool TWO>
-__global__ __launch_bounds__(kThreads) void k_distill_sums(Args a) {
-  extern __shared__ uint32_t bits[];  // TAIL: span / 32 words
-  __shared__ float red[3][kThreads / 64];
-  const int64_t row = blockIdx.x / a.split;
-  const int part = (int)(blockIdx.x % a.split);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->epoch = a.epoch;
-  if (weight_of(a, row) == 0.f) return;  // padding: not read
-  const int64_t c0 = (int64_t)part * a.span, c1 = min(a.V, c0 + a.span);
-  const T* x = static_cast<const T*>(a.logits) + row * a.sl;
-  if (TAIL) {
-    for (int i = threadIdx.x; i < a.span / 32; i += kThreads) bits[i] = 0;
-    __syncthreads();
-    mark_listed(a, row, c0, c1, bits);
-    __syncthreads();
-  }
+// The workgroup's sums over columns [c0, c1) (those without a bit), the same
+// in every lane.
+template <typename T, bool TAIL, bool TWO, int NT>
+__device__ __forceinline__ float4 sums_of(const Args& a, const T* x, uint32_t c0, uint32_t c1,
+                                          const uint32_t* bits, float (*red)[NT / 64]) {
   Sums<TWO> sum;
-#pragma unroll 2
-  for (int64_t col = c0 + threadIdx.x * 8; col < c1; col += kStep) {
-    const int n = (int)min((int64_t)8, c1 - col);
-    const Raw8<T> raw = load8(x + col, n);
+  stream<NT>(x, c0, c1, (uint32_t)a.V, [&](const Raw8<T>& r, uint32_t col, int n) {
+    if (n <= 0) return;
     float v[8];
-    widen8(raw, v);
-    if (n < 8) {
+    widen8(r, v);
+    uint32_t skip = n < 8 ? 0xffu << n & 0xffu : 0u;
+    if (TAIL) skip |= reinterpret_cast<const uint8_t*>(bits)[(col - c0) >> 3];
+    if (skip) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i >= n) v[i] = -INFINITY;
-    }
-    if (TAIL) {
-      const uint32_t skip = reinterpret_cast<const uint8_t*>(bits)[(col - c0) >> 3];
-      if (skip) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (skip >> i & 1) v[i] = -INFINITY;
-      }
+        if (skip >> i & 1) v[i] = -INFINITY;
     }
     sum.add(v, a.c);
-  }
+  });
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float top = wave_max(sum.m);
   sum.scale_to(top, a.c);
@@ -158,16 +174,36 @@ __global__ __launch_bounds__(kThreads) void k_distill_sums(Args a) {
     red[2][wave] = s1;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float m = red[0][0];
-    for (int w = 1; w < kThreads / 64; ++w) m = fmaxf(m, red[0][w]);
-    float4 o = make_float4(m, 0.f, 0.f, 0.f);
-    for (int w = 0; w < kThreads / 64; ++w) {
-      o.y += red[1][w] * exp2_of((red[0][w] - m) * a.c);
-      o.z += red[2][w] * exp2_of((red[0][w] - m) * kLog2e);
-    }
-    a.part[row * a.split + part] = o;
+  float m = red[0][0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) m = fmaxf(m, red[0][w]);
+  float4 o = make_float4(m, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) {
+    o.y += red[1][w] * exp2_of((red[0][w] - m) * a.c);
+    if (TWO) o.z += red[2][w] * exp2_of((red[0][w] - m) * kLog2e);
   }
+  return o;
+}
+
+template <typename T, bool TAIL, bool TWO>
+__global__ __launch_bounds__(kThreads) void k_distill_sums(Args a) {
+  extern __shared__ uint32_t bits[];  // TAIL: span / 32 words
+  __shared__ float red[3][kThreads / 64];
+  const int64_t row = blockIdx.x / (uint32_t)a.split;
+  const int part = (int)(blockIdx.x % (uint32_t)a.split);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->epoch = a.epoch;
+  if (weight_of(a, row) == 0.f) return;  // padding: not read
+  const int64_t c0 = (int64_t)part * a.span, c1 = min(a.V, c0 + a.span);
+  const T* x = static_cast<const T*>(a.logits) + row * a.sl;
+  if (TAIL) {
+    for (int i = threadIdx.x; i < a.span / 32; i += kThreads) bits[i] = 0;
+    __syncthreads();
+    mark_listed<kThreads>(a, row, c0, c1, bits);
+    __syncthreads();
+  }
+  const float4 o = sums_of<T, TAIL, TWO, kThreads>(a, x, (uint32_t)c0, (uint32_t)c1, bits, red);
+  if (threadIdx.x == 0) a.part[row * a.split + part] = o;
 }
 
 // ------------------------------------------------------------- listed terms
@@ -468,20 +504,37 @@ __device__ __forceinline__ void patch(const Args& a, int64_t row, int64_t c0, in
   }
 }
 
+template <typename T, bool TWO, int NT>
+__device__ __forceinline__ void write_gradient(const Args& a, const T* x, T* grad, uint32_t c0,
+                                               uint32_t c1, const Terms& t) {
+  const float m = t.m, ca = t.ca, cb = t.cb;
+  stream<NT>(x, c0, c1, (uint32_t)a.V, [&](const Raw8<T>& r, uint32_t col, int n) {
+    if (n <= 0) return;
+    float v[8];
+    widen8(r, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = v[i] - m;
+      float g = ca * exp2_of(d * a.c);
+      if (TWO) g = fmaf(cb, exp2_of(d * kLog2e), g);
+      v[i] = g;
+    }
+    store8(grad, col, v, n);
+  });
+}
+
 template <typename T, bool TAIL, bool TWO>
 __global__ __launch_bounds__(kThreads) void k_distill_grad(Args a) {
   extern __shared__ char lds[];
   __shared__ Terms t;
-  const int64_t row = blockIdx.x / a.split;
-  const int part = (int)(blockIdx.x % a.split);
+  const int64_t row = blockIdx.x / (uint32_t)a.split;
+  const int part = (int)(blockIdx.x % (uint32_t)a.split);
   if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->epoch = a.epoch;
   const int64_t c0 = (int64_t)part * a.span, c1 = min(a.V, c0 + a.span);
   const T* x = static_cast<const T*>(a.logits) + row * a.sl;
   T* grad = static_cast<T*>(a.grad) + row * a.sg;
   if (weight_of(a, row) == 0.f) {
-    const float zero[8] = {};
-    for (int64_t col = c0 + threadIdx.x * 8; col < c1; col += kStep)
-      store8(grad + col, zero, (int)min((int64_t)8, c1 - col));
+    write_zeros<kThreads>(grad, (uint32_t)c0, (uint32_t)c1);
     if (a.loss && part == 0 && threadIdx.x == 0) a.loss[row] = 0.f;
     return;
   }
@@ -499,217 +552,76 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(Args a) {
     }
   }
   __syncthreads();
-  const float m = t.m, ca = t.ca, cb = t.cb;
-#pragma unroll 2
-  for (int64_t col = c0 + threadIdx.x * 8; col < c1; col += kStep) {
-    const int n = (int)min((int64_t)8, c1 - col);
-    float v[8];
-    widen8(load8(x + col, n), v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = v[i] - m;
-      float g = ca * exp2_of(d * a.c);
-      if (TWO) g = fmaf(cb, exp2_of(d * kLog2e), g);
-      v[i] = g;
-    }
-    store8(grad + col, v, n);
-  }
+  write_gradient<T, TWO, kThreads>(a, x, grad, (uint32_t)c0, (uint32_t)c1, t);
   __syncthreads();  // the stream's stores come before the patch's
   if (threadIdx.x < 64) patch<T, TAIL>(a, row, c0, c1, t, l);
 }
 
-// ------------------------------------------------------------- a row at once
+// ------------------------------------------------------------- a row a workgroup
 //
-// Loss and gradient of rows that a workgroup's registers can hold (up to 128
-// logits of 16 bits a lane, 64 of 32): read once, their maximum, the sums
-// relative to it, the terms, and the gradient from the same registers.  The
-// workgroup stays for several rows: as a part of the gradient is stored, the
-// next row's logits are asked for in its place, and the last wave gathers the
-// next row's listed terms meanwhile.
+// Where there are rows enough, a workgroup takes a whole row: the sums, the
+// terms and (GRAD) the gradient.  The gradient's reading of the logits comes
+// from the caches: at two workgroups of 1024 lanes a compute unit the rows in
+// flight, 256 KB each, fit in the last level's 256 MB (of 4096 rows of 131072
+// bf16, counters: 0.95 GB fetched and 1.08 GB written).
+//
+// Measured on those, with a tail and labels: 454 us, against 608 for the sums
+// and the gradient in launches of their own and 534 for rows held in 256
+// registers a lane (read once, but a row a compute unit leaves nothing to do
+// while its terms are found).  1024 lanes 454 us, 512 494, 256 598; on 2048
+// rows of 8000 columns 52, 33 and 23 us.
 
-// The listed ids of a row in the bits (one wave); `on` false takes them out.
-__device__ __forceinline__ void mark_wave(const Args& a, const Listed& l, uint32_t* bits, bool on) {
-  for (int k = threadIdx.x & 63; k < a.K; k += 64) {
-    const int id = l.id[k];
-    if (id < 0) continue;
-    if (on)
-      atomicOr(&bits[id >> 5], 1u << (id & 31));
-    else
-      bits[id >> 5] = 0;
-  }
-}
-
-template <int NT, typename F>
-__device__ __forceinline__ float block_fold(float x, float* red, F f) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  x = wave_fold(x, 64, f);
-  if (lane == 0) red[wave] = x;
-  __syncthreads();
-  x = red[lane % (NT / 64)];
-  return wave_fold(x, NT / 64 < 8 ? 8 : NT / 64, f);
-}
-
-// Keeps the compiler from holding what it made of the registers in one pass
-// (the same logits in fp32, twice their size) for the next.
-template <typename T>
-__device__ __forceinline__ void forget(Raw8<T>& r) {
-#pragma unroll
-  for (int i = 0; i < Vec<T>::kWords; ++i) asm volatile("" : "+v"(r.w[i]));
-}
-
-template <typename T, bool TAIL, bool TWO, int NT, int NC>
-__global__ __launch_bounds__(NT, 2) void k_distill_row(Args a) {
+template <typename T, bool TAIL, bool TWO, bool GRAD, int NT>
+__global__ __launch_bounds__(NT) void k_distill_row(Args a) {
   extern __shared__ char lds[];
   __shared__ Terms terms;
-  __shared__ Known known[2];
+  __shared__ Known known;
   __shared__ float red[3][NT / 64];
   const int t = (int)threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  constexpr int kLast = NT / 64 - 1;
-  uint32_t* bits = reinterpret_cast<uint32_t*>(lds);  // TAIL: a bit a logit
-  char* lists = lds + (TAIL ? a.span / 8 : 0);
-  const int list_bytes = (int)listed_bytes(a.K, a.table);
-  if (blockIdx.x == 0 && t == 0) a.hdr->epoch = a.epoch;
+  const int64_t row = blockIdx.x;
+  if (row == 0 && t == 0) a.hdr->epoch = a.epoch;
+  T* grad = static_cast<T*>(a.grad) + row * a.sg;
+  float4* stats = reinterpret_cast<float4*>(a.stats);
   const uint32_t V = (uint32_t)a.V;
-
-  // the next row at or after `row` that counts; padding rows are written on the way
-  auto settle = [&](int64_t row) {
-    while (row < a.rows && weight_of(a, row) == 0.f) {
-      T* grad = static_cast<T*>(a.grad) + row * a.sg;
-      const float zero[8] = {};
-      for (uint32_t col = t * 8; col < V; col += NT * 8) store8(grad + col, zero, (int)min(8u, V - col));
-      if (t == 0) a.loss[row] = 0.f;
-      row += gridDim.x;
+  if (weight_of(a, row) == 0.f) {
+    if (GRAD) write_zeros<NT>(grad, 0, V);
+    if (t == 0) {
+      a.loss[row] = 0.f;
+      if (stats) stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    return row;
-  };
-
-  int64_t row = settle(blockIdx.x);
-  if (row >= a.rows) return;
-  Raw8<T> raw[NC];
+    return;
+  }
   const T* x = static_cast<const T*>(a.logits) + row * a.sl;
-#pragma unroll
-  for (int c = 0; c < NC; ++c) raw[c] = ask8(x, (c * NT + t) * 8, V);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(lds);
+  const Listed l = listed_in(lds + (TAIL ? a.span / 8 : 0), a.K);
   if (TAIL) {
     for (int i = t; i < a.span / 32; i += NT) bits[i] = 0;
     __syncthreads();
+    mark_listed<NT>(a, row, 0, V, bits);
+    __syncthreads();
   }
-  int par = 0;
-  if (wave == kLast) {
-    const Listed l = listed_in(lists, a.K);
+  if (wave == NT / 64 - 1) {
     Known n;
     gather<T, TAIL, TWO>(a, row, l, n);
-    if (TAIL) mark_wave(a, l, bits, true);
-    if ((t & 63) == 0) known[0] = n;
+    if ((t & 63) == 0) known = n;
   }
+  const float4 sums = sums_of<T, TAIL, TWO, NT>(a, x, 0, V, bits, red);
+  if (wave == 0) {
+    Terms mine;
+    double loss;
+    finish<TAIL, TWO>(a, known, sums, mine, loss);
+    if (t == 0) {
+      terms = mine;
+      a.loss[row] = (float)loss;
+      if (stats) stats[row] = sums;
+    }
+  }
+  if (!GRAD) return;
   __syncthreads();
-
-  while (true) {
-    // the largest, with what is left out set to -inf
-    float top = -FLT_MAX;
-    int at = t * 8;
-    asm volatile("" : "+v"(at));  // not kept in registers for every part
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int col = c * NT * 8 + at, n = (int)V - col;
-      if (n < 8) have8(raw[c], n);
-      uint32_t skip = n < 8 ? (n > 0 ? 0xffu << n : 0xffu) & 0xffu : 0u;
-      if (TAIL && n > 0) skip |= reinterpret_cast<const uint8_t*>(bits)[col >> 3];
-      if (skip) {
-        constexpr int W = Vec<T>::kWords;
-        constexpr uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : __is_same(T, bf16_t) ? 0xff80u : 0xfc00u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (W == 8) {
-            raw[c].w[i] = skip >> i & 1 ? ninf : raw[c].w[i];
-          } else {
-            const uint32_t keep = i & 1 ? 0xffffu : 0xffff0000u;
-            const uint32_t w = (raw[c].w[i >> 1] & keep) | (ninf << (16 * (i & 1)));
-            raw[c].w[i >> 1] = skip >> i & 1 ? w : raw[c].w[i >> 1];
-          }
-        }
-      }
-      float v[8];
-      widen8(raw[c], v);
-      top = fmaxf(fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])),
-                        fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7]))), top);
-    }
-    top = block_fold<NT>(top, red[0], [](float p, float q) { return fmaxf(p, q); });
-    float s = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float v[8], p[8];
-      forget(raw[c]);
-      widen8(raw[c], v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = exp2_of((v[i] - top) * a.c);
-      s += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-      if (TWO) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = exp2_of((v[i] - top) * kLog2e);
-        s1 += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-      }
-    }
-    auto add = [](float p, float q) { return p + q; };
-    const int lane = t & 63;
-    s = wave_fold(s, 64, add);
-    if (TWO) s1 = wave_fold(s1, 64, add);
-    if (lane == 0) {
-      red[1][wave] = s;
-      red[2][wave] = s1;
-    }
-    __syncthreads();
-    if (wave == 0) {
-      s = s1 = 0.f;
-      for (int w = 0; w < NT / 64; ++w) s += red[1][w], s1 += red[2][w];
-      Terms mine;
-      double loss;
-      finish<TAIL, TWO>(a, known[par], make_float4(top, s, s1, 0.f), mine, loss);
-      if (t == 0) {
-        terms = mine;
-        a.loss[row] = (float)loss;
-      }
-    }
-    __syncthreads();
-
-    const int64_t next = settle(row + gridDim.x);
-    const bool more = next < a.rows;
-    if (more && wave == kLast) {
-      const Listed l = listed_in(lists + (par ^ 1) * list_bytes, a.K);
-      if (TAIL) mark_wave(a, listed_in(lists + par * list_bytes, a.K), bits, false);
-      Known n;
-      gather<T, TAIL, TWO>(a, next, l, n);
-      if (TAIL) mark_wave(a, l, bits, true);
-      if (lane == 0) known[par ^ 1] = n;
-    }
-    const float m = terms.m, ca = terms.ca, cb = terms.cb;
-    T* grad = static_cast<T*>(a.grad) + row * a.sg;
-    x = static_cast<const T*>(a.logits) + next * a.sl;
-    at = t * 8;
-    asm volatile("" : "+v"(at));
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int col = c * NT * 8 + at;
-      float v[8];
-      forget(raw[c]);
-      widen8(raw[c], v);
-      if (more) raw[c] = ask8(x, col, V);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = v[i] - m;
-        float g = ca * exp2_of(d * a.c);
-        if (TWO) g = fmaf(cb, exp2_of(d * kLog2e), g);
-        v[i] = g;
-      }
-      store8(grad, (uint32_t)col, v, (int)V - col);
-    }
-    __syncthreads();  // the stream's stores come before the patch's
-    if (wave == 0)
-      patch<T, TAIL>(a, row, 0, a.V, terms, listed_in(lists + par * list_bytes, a.K));
-    if (!more) return;
-    row = next;
-    par ^= 1;
-  }
+  write_gradient<T, TWO, NT>(a, x, grad, 0, V, terms);
+  __syncthreads();  // the stream's stores come before the patch's
+  if (wave == 0) patch<T, TAIL>(a, row, 0, a.V, terms, l);
 }
 
 }  // namespace
@@ -736,36 +648,42 @@ int split_of(const sgb_distill_s* p, int64_t rows) {
 
 enum What { kLoss, kBackward, kBoth };
 
-template <typename T, bool TAIL, bool TWO, int NT, int NC>
-void run_rows(Args a, int cus, hipStream_t s) {
+template <typename T, bool TAIL, bool TWO, bool GRAD, int NT>
+void run_rows(Args a, hipStream_t s) {
   a.span = (int)align_up((size_t)a.V, 32);
-  const int64_t grid = std::min(a.rows, (int64_t)cus * (NT == 512 ? 1 : NC * sizeof(T) >= 64 ? 2 : 3));
-  const size_t lds = (TAIL ? a.span / 8 : 0) + 2 * listed_bytes(a.K, a.table);
-  hipLaunchKernelGGL((k_distill_row<T, TAIL, TWO, NT, NC>), dim3((unsigned)grid), dim3(NT), lds, s, a);
+  const size_t lds = (TAIL ? a.span / 8 : 0) + listed_bytes(a.K, a.table);
+  hipLaunchKernelGGL((k_distill_row<T, TAIL, TWO, GRAD, NT>), dim3((unsigned)a.rows), dim3(NT), lds,
+                     s, a);
 }
 
-// Does a row of V logits of T fit in a workgroup's registers, and are there
-// rows enough to fill the card a workgroup a row?
-template <typename T>
-bool at_once(const Args& a, int cus) {
-  return a.V >= 8 && a.V <= (sizeof(T) == 4 ? 65536 : 131072) && a.K <= 512 && a.rows >= SGB_ROWMIN;
+// The longer the row, the more lanes: few rows in flight are long enough to
+// keep the memory busy, and they have to fit in the caches.
+template <typename T, bool TAIL, bool TWO, bool GRAD>
+void run_rows(const Args& a, hipStream_t s) {
+  const size_t bytes = (size_t)a.V * sizeof(T);
+  if (bytes <= kShortRow)
+    run_rows<T, TAIL, TWO, GRAD, 256>(a, s);
+  else if (bytes <= 4 * kShortRow)
+    run_rows<T, TAIL, TWO, GRAD, 512>(a, s);
+  else
+    run_rows<T, TAIL, TWO, GRAD, 1024>(a, s);
+}
+
+// A row a workgroup, or several workgroups a row and the loss in a launch of
+// its own?  (Loss and gradient: 64 rows of 131072 bf16 take 17 us in parts and
+// 25 as rows, 128 take 26.5 and 26.8, 256 take 43 and 38; of 8000 columns 1 row
+// takes 10.1 and 9.5.)
+bool rows_at_once(const Args& a, size_t elem, int cus) {
+  return a.V <= kMaxSpan && (a.rows >= cus / 2 || (size_t)a.V * elem <= kShortRow);
 }
 
 template <typename T, bool TAIL, bool TWO>
 void run_as(const Args& a, What what, int cus, hipStream_t s) {
-  if (what == kBoth && at_once<T>(a, cus)) {
-    if (a.V <= 8192)
-      run_rows<T, TAIL, TWO, 256, 4>(a, cus, s);
-    else if (a.V <= 16384)
-      run_rows<T, TAIL, TWO, 256, 8>(a, cus, s);
-    else if (a.V <= 32768)
-      run_rows<T, TAIL, TWO, 256, 16>(a, cus, s);
-    else if constexpr (sizeof(T) == 4)
-      run_rows<T, TAIL, TWO, 512, 16>(a, cus, s);
-    else if (a.V <= 65536)
-      run_rows<T, TAIL, TWO, 256, 32>(a, cus, s);
+  if (what != kBackward && rows_at_once(a, sizeof(T), cus)) {
+    if (what == kBoth)
+      run_rows<T, TAIL, TWO, true>(a, s);
     else
-      run_rows<T, TAIL, TWO, 512, 32>(a, cus, s);
+      run_rows<T, TAIL, TWO, false>(a, s);
     return;
   }
   const dim3 grid((unsigned)(a.rows * a.split));
