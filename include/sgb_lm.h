@@ -49,7 +49,8 @@ extern "C" {
 /*
  * sgb_lm_device_status -- synchronises `stream`, then stores in *out the
  * first error the kernels of the last call that used `workspace` recorded
- * (SGB_OK if none).  Distillation and penalties record
+ * (SGB_OK if none; the replays of a captured call count as one call).
+ * Distillation and penalties record
  * SGB_ERR_INDEX_OUT_OF_RANGE (an entry, label, token, bias id or mask index
  * at or past its range; it is left out and the rest computed) and
  * SGB_ERR_BAD_OFFSETS (a length outside its range; it is clamped).

@@ -318,13 +318,16 @@ int compute_units(int device);
 
 struct DeviceGuard {
   int prev = -1;
-  bool ok = false;
+  bool ok = false, changed = false;
   explicit DeviceGuard(int dev) {
     if (dev < 0 || hipGetDevice(&prev) != hipSuccess) return;
-    ok = prev == dev || hipSetDevice(dev) == hipSuccess;
+    if (prev == dev)
+      ok = true;
+    else
+      ok = changed = hipSetDevice(dev) == hipSuccess;
   }
   ~DeviceGuard() {
-    if (ok && prev >= 0) (void)hipSetDevice(prev);
+    if (changed) (void)hipSetDevice(prev);
   }
 };
 

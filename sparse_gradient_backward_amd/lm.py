@@ -81,10 +81,17 @@ def _bad(where: str, what: str):
     raise SgbError(SGB_ERR_INVALID_ARGUMENT, f"{where}: {what}")
 
 
-def _stream(stream, device) -> int:
-    if device.type != "cuda":
+# The current stream's handle without the Stream object that
+# torch.cuda.current_stream() makes of it (2 us, half a one-token kernel's time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, index) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if index < 0:
         return 0
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
 
 
 class _Plan:
@@ -99,6 +106,7 @@ class _Plan:
         # without a GPU a plan checks arguments and its calls end in SGB_ERR_HIP
         self._device = torch.device("cuda", torch.cuda.current_device()) \
             if torch.cuda.is_available() else torch.device("cpu")
+        self._index = -1 if self._device.type == "cpu" else self._device.index
 
     def workspace_bytes(self, rows: int) -> int:
         n = _sz()
@@ -113,7 +121,7 @@ class _Plan:
     def device_status(self, workspace, stream=None) -> str:
         """Waits for `stream`; the first error that the last call on `workspace` recorded."""
         out = _i32()
-        _check(_lib.sgb_lm_device_status(workspace.data_ptr(), _stream(stream, self._device),
+        _check(_lib.sgb_lm_device_status(workspace.data_ptr(), _stream(stream, self._index),
                                          ctypes.byref(out)), "sgb_lm_device_status")
         return sgb_status_string(out.value)
 
@@ -121,27 +129,29 @@ class _Plan:
         """Pointer and row stride of a 2-D argument (None: 0, 0)."""
         if t is None:
             return 0, 0
-        s = t.stride()
-        if t.dtype != dtype or t.shape != shape or (s[1] != 1 and shape[1] > 1):
+        if t.shape != shape or t.dtype is not dtype:
             _bad(where, f"{name} must be {list(shape)} {dtype} with adjacent row elements")
-        if t.device != self._device:
+        pitch, step = t.stride()
+        if step != 1 and shape[1] > 1:
+            _bad(where, f"{name} must be {list(shape)} {dtype} with adjacent row elements")
+        if t.get_device() != self._index:
             _bad(where, f"{name} must be on {self._device}")
         # the stride of a single row says nothing
-        return t.data_ptr(), (s[0] if shape[0] > 1 else max(s[0], shape[1]))
+        return t.data_ptr(), (pitch if shape[0] > 1 else max(pitch, shape[1]))
 
     def _vector(self, name, t, dtype, n, where):
         if t is None:
             return 0
-        if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
             _bad(where, f"{name} must be contiguous {dtype} of {n} elements")
-        if t.device != self._device:
+        if t.get_device() != self._index:
             _bad(where, f"{name} must be on {self._device}")
         return t.data_ptr()
 
     def _space(self, ws, where):
         if ws is None:
             _bad(where, "workspace is missing")
-        if ws.device != self._device or not ws.is_contiguous():
+        if ws.get_device() != self._index or not ws.is_contiguous():
             _bad(where, f"workspace must be contiguous on {self._device}")
         return ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -176,11 +186,15 @@ class BlockNorm(_Plan):
 
     def _params(self, where):
         ps = (self.post_weight, self.post_bias, self.pre_weight, self.pre_bias)
-        dtype = next((p.dtype for p in ps if p is not None), torch.float32)
+        dtype, at = None, [0, 0, 0, 0]
+        for i, p in enumerate(ps):
+            if p is not None:
+                dtype = dtype or p.dtype
+                at[i] = self._vector("a parameter", p, dtype, self.D, where)
+        dtype = dtype or torch.float32
         if dtype not in _DTYPE:
             _bad(where, f"parameters cannot be {dtype}")
-        return _NORM_PARAMS.pack(*[self._vector("a parameter", p, dtype, self.D, where)
-                                   for p in ps], _DTYPE[dtype])
+        return _NORM_PARAMS.pack(*at, _DTYPE[dtype])
 
     def _types(self, x, h, where):
         if x is None or h is None or h.dtype not in _DTYPE or x.dtype not in _DTYPE:
@@ -213,7 +227,7 @@ class BlockNorm(_Plan):
             _NORM_FORWARD.pack(px, ph, po, py, pg,
                                self._vector("stats", stats, torch.float32, 4 * rows, w),
                                sx, sh, so, sy, sg, rows, rpg, _DTYPE[dt], _DTYPE[rt]),
-            _stream(stream, self._device))
+            _stream(stream, self._index))
         _check(st, w)
 
     def backward(self, dx_out, dy, x_out, h, stats, dx, dh, gate=None, rows_per_gate: int = 1,
@@ -245,7 +259,7 @@ class BlockNorm(_Plan):
             _NORM_BACKWARD.pack(pdxo, pdy, px, ph, self._vector("stats", stats, f32, 4 * rows, w),
                                 pg, pdx, pdh, pdg, *vec, sdxo, sdy, sx, sh, sg, sdx, sdh, sdg,
                                 rows, rpg, _DTYPE[dt], _DTYPE[rt]),
-            ws, ws_bytes, _stream(stream, self._device))
+            ws, ws_bytes, _stream(stream, self._index))
         _check(st, w)
 
 
@@ -281,7 +295,7 @@ class TopkDistill(_Plan):
             sl, si, sv, sg, rows, _DTYPE[dt], grad_scale)
         ws, ws_bytes = self._space(workspace, name)
         _check(getattr(_lib, name)(self.handle, args, ws, ws_bytes,
-                                   _stream(stream, self._device)), name)
+                                   _stream(stream, self._index)), name)
 
     def forward(self, logits, ids, values, loss, stats=None, teacher_lse=None, labels=None,
                 row_weights=None, workspace=None, stream=None) -> None:
@@ -358,4 +372,4 @@ class LogitsPenalty(_Plan):
             sl, so, st_, sbi, sb, sm, rows, L, n, masks, _DTYPE[dt])
         ws, ws_bytes = self._space(workspace, w)
         _check(_lib.sgb_penalty_apply(self.handle, args, ws, ws_bytes,
-                                      _stream(stream, self._device)), w)
+                                      _stream(stream, self._index)), w)

@@ -230,3 +230,30 @@ def test_differences(lm):
         return o.double()
     num = (at(cu["x"] + e * grad / n) - at(cu["x"] - e * grad / n)) / (2 * e)
     assert torch.allclose(num, n[:, 0].double(), rtol=1e-2)
+
+
+@pytest.mark.parametrize("V,dt", [(20011, "f16"), (16390, "bf16"), (70001, "bf16"), (34003, "f32")])
+def test_a_row_a_workgroup(lm, V, dt):
+    """Rows enough for a workgroup each, of lengths either side of where its
+    width changes (32 and 128 KB); a few of them padding."""
+    c = make(131, V, 6, dt, 1.5, True, 0.3)
+    c["w"][5:9] = 0
+    run(lm, c, 1.5, 0.7, 0.3, "rows")
+
+
+def test_a_row_a_workgroup_without_a_tail(lm):
+    c = make(130, 17001, 40, "f32", 1.0, False, 0.0)
+    c["ids"][3] = -1
+    run(lm, c, 1.0, 1.0, 0.0, "rows without a tail")
+
+
+def test_stats_of_padding_rows(lm):
+    """Forward writes them all, in parts and as rows."""
+    for rows in (4, 130):
+        c = make(rows, 20000, 4, "bf16", 1.0, False, 0.0)
+        c["w"][1] = 0
+        d = lm.TopkDistill(20000, 4)
+        loss, st = torch.full((rows,), 7.0, device="cuda"), torch.full((rows, 4), torch.nan, device="cuda")
+        d.forward(c["x"].cuda(), c["ids"].cuda(), c["vals"].cuda(), loss, stats=st,
+                  row_weights=c["w"].cuda(), workspace=d.workspace(rows))
+        assert bool(st.isfinite().all()) and float(loss[1]) == 0 and not bool(st[1].any())

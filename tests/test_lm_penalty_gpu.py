@@ -187,3 +187,18 @@ def test_strides(lm):
             mask=wide(cu["mask"], 0, 40)[0], **kw)
     assert torch.equal(o, out)
     assert bool((wo[:, :7] == 3).all()) and bool((wo[:, 7 + V:] == 3).all())
+
+
+@pytest.mark.parametrize("L", [8191, 8192, 8193, 16385, 40001])
+def test_long_sequences(lm, L):
+    """Either side of what one round of token loads holds."""
+    c = make(2, 1500, L, 3, 0, "bf16")
+    c["lens"][1] = L - 1
+    c["prompt"][1] = L // 2
+    run(lm, c, "long")
+
+
+@pytest.mark.parametrize("V", [8193, 8199, 16385, 24571])
+def test_last_slices(lm, V):
+    """A last slice of one logit, of seven, of whole vectors and a part."""
+    assert run(lm, make(300, V, 12, 4, 3, "f16"), in_place=True) == "SGB_OK"
