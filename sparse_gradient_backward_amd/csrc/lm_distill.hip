@@ -101,13 +101,19 @@ struct Sums {
 
 // f(eight logits as loaded, column) over columns [c0, c1) of a row, kAhead
 // loads of a lane in flight.  Every lane makes every turn; f looks at the column.
+#ifndef ASIDE
+#define ASIDE 64
+#endif
 constexpr int kAhead = 2;
 
-template <int NT, typename T, typename F>
-__device__ __forceinline__ void stream(const T* row, uint32_t c0, uint32_t c1, uint32_t V, F f) {
+// `meanwhile` is called with the first loads on their way.
+template <int NT, typename T, typename F, typename G>
+__device__ __forceinline__ void stream(const T* row, uint32_t c0, uint32_t c1, uint32_t V, F f,
+                                       G meanwhile) {
   constexpr uint32_t kStride = NT * 8;
   uint32_t col = c0 + threadIdx.x * 8;
   if (V < 8) {  // a load of eight does not fit
+    meanwhile();
     const int n = (int)V - (int)col;
     f(load8(row + col, n), col, n);
     return;
@@ -115,6 +121,7 @@ __device__ __forceinline__ void stream(const T* row, uint32_t c0, uint32_t c1, u
   Raw8<T> q[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) q[u] = ask8(row, col + u * kStride, c1);
+  meanwhile();
   for (uint32_t base = c0; base < c1; base += kAhead * kStride) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -146,12 +153,19 @@ __device__ __forceinline__ void mark_listed(const Args& a, int64_t row, int64_t 
 }
 
 // The workgroup's sums over columns [c0, c1) (those without a bit), the same
-// in every lane.
-template <typename T, bool TAIL, bool TWO, int NT>
+// in every lane: the first NS lanes read the logits, the others do `aside`
+// instead.
+template <typename T, bool TAIL, bool TWO, int NT, int NS, typename G, typename H>
 __device__ __forceinline__ float4 sums_of(const Args& a, const T* x, uint32_t c0, uint32_t c1,
-                                          const uint32_t* bits, float (*red)[NT / 64]) {
+                                          const uint32_t* bits, float (*red)[NT / 64], G meanwhile,
+                                          H aside) {
   Sums<TWO> sum;
-  stream<NT>(x, c0, c1, (uint32_t)a.V, [&](const Raw8<T>& r, uint32_t col, int n) {
+  const bool streams = NS == NT || __builtin_amdgcn_readfirstlane(threadIdx.x) < NS;
+  if (!streams) {
+    meanwhile();
+    aside();
+  } else {
+  stream<NS>(x, c0, c1, (uint32_t)a.V, [&](const Raw8<T>& r, uint32_t col, int n) {
     if (n <= 0) return;
     float v[8];
     widen8(r, v);
@@ -163,7 +177,8 @@ __device__ __forceinline__ float4 sums_of(const Args& a, const T* x, uint32_t c0
         if (skip >> i & 1) v[i] = -INFINITY;
     }
     sum.add(v, a.c);
-  });
+  }, meanwhile);
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float top = wave_max(sum.m);
   sum.scale_to(top, a.c);
@@ -196,13 +211,15 @@ __global__ __launch_bounds__(kThreads) void k_distill_sums(Args a) {
   if (weight_of(a, row) == 0.f) return;  // padding: not read
   const int64_t c0 = (int64_t)part * a.span, c1 = min(a.V, c0 + a.span);
   const T* x = static_cast<const T*>(a.logits) + row * a.sl;
-  if (TAIL) {
+  auto mark = [&] {
+    if (!TAIL) return;
     for (int i = threadIdx.x; i < a.span / 32; i += kThreads) bits[i] = 0;
     __syncthreads();
     mark_listed<kThreads>(a, row, c0, c1, bits);
     __syncthreads();
-  }
-  const float4 o = sums_of<T, TAIL, TWO, kThreads>(a, x, (uint32_t)c0, (uint32_t)c1, bits, red);
+  };
+  const float4 o = sums_of<T, TAIL, TWO, kThreads, kThreads>(
+      a, x, (uint32_t)c0, (uint32_t)c1, bits, red, mark, [] {});
   if (threadIdx.x == 0) a.part[row * a.split + part] = o;
 }
 
@@ -218,6 +235,7 @@ struct Terms {
   float ca, cb;               // gradient: ca exp((x-m)/T) + cb exp(x-m)
   float above;                // row weight, scale and gradient from above
   int64_t label;              // -1: none
+  float label_x;
   int repeated;               // some id is listed twice
 };
 
@@ -378,6 +396,7 @@ __device__ __forceinline__ void finish(const Args& a, const Known& n, float4 sum
   o.above = n.above;
   o.repeated = n.repeated;
   o.label = n.label;
+  o.label_x = n.label_x;
   o.base = m;
   o.lse = log(s);
   o.lse_out = TAIL ? ((double)sums.x - m) * invT + log_out : o.lse;
@@ -484,11 +503,21 @@ __device__ __forceinline__ float label_grad(const Args& a, const Terms& t, float
                                     (double)a.ce * (exp(x - t.lse1) - 1.0)));
 }
 
-// Writes over columns [c0, c1) of the gradient what the stream could not know
-// (one wave, after the stream's stores).
-template <typename T, bool TAIL>
+// What the stream cannot know of the gradient (one wave): the listed ids', left
+// in place of their logits, and the label's.
+template <bool TAIL>
+__device__ __forceinline__ float listed_grads(const Args& a, const Terms& t, const Listed& l) {
+  const int lane = threadIdx.x & 63;
+  const float at_label = t.label >= 0 ? label_grad<TAIL>(a, t, t.label_x) : 0.f;
+  for (int k = lane; k < a.K; k += 64)
+    if (l.owner[k]) l.x[k] = listed_grad(a, t, l, k);
+  return at_label;
+}
+
+// Writes it over columns [c0, c1), after the stream's stores.
+template <typename T>
 __device__ __forceinline__ void patch(const Args& a, int64_t row, int64_t c0, int64_t c1,
-                                      const Terms& t, const Listed& l) {
+                                      const Terms& t, const Listed& l, float at_label) {
   const int lane = threadIdx.x & 63;
   T* grad = static_cast<T*>(a.grad) + row * a.sg;
   bool label_listed = false;
@@ -496,12 +525,10 @@ __device__ __forceinline__ void patch(const Args& a, int64_t row, int64_t c0, in
     if (!l.owner[k]) continue;
     const int64_t id = l.id[k];
     label_listed |= id == t.label;
-    if (id >= c0 && id < c1) grad[id] = (T)listed_grad(a, t, l, k);
+    if (id >= c0 && id < c1) grad[id] = (T)l.x[k];
   }
-  if (t.label >= c0 && t.label < c1 && !__ballot(label_listed) && lane == 0) {
-    const T* x = static_cast<const T*>(a.logits) + row * a.sl;
-    grad[t.label] = (T)label_grad<TAIL>(a, t, widen(x[t.label]));
-  }
+  if (t.label >= c0 && t.label < c1 && !__ballot(label_listed) && lane == 0)
+    grad[t.label] = (T)at_label;
 }
 
 template <typename T, bool TWO, int NT>
@@ -520,7 +547,7 @@ __device__ __forceinline__ void write_gradient(const Args& a, const T* x, T* gra
       v[i] = g;
     }
     store8(grad, col, v, n);
-  });
+  }, [] {});
 }
 
 template <typename T, bool TAIL, bool TWO>
@@ -553,8 +580,9 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(Args a) {
   }
   __syncthreads();
   write_gradient<T, TWO, kThreads>(a, x, grad, (uint32_t)c0, (uint32_t)c1, t);
+  const float at_label = threadIdx.x < 64 ? listed_grads<TAIL>(a, t, l) : 0.f;
   __syncthreads();  // the stream's stores come before the patch's
-  if (threadIdx.x < 64) patch<T, TAIL>(a, row, c0, c1, t, l);
+  if (threadIdx.x < 64) patch<T>(a, row, c0, c1, t, l, at_label);
 }
 
 // ------------------------------------------------------------- a row a workgroup
@@ -595,18 +623,21 @@ __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
   const T* x = static_cast<const T*>(a.logits) + row * a.sl;
   uint32_t* bits = reinterpret_cast<uint32_t*>(lds);
   const Listed l = listed_in(lds + (TAIL ? a.span / 8 : 0), a.K);
-  if (TAIL) {
+  auto mark = [&] {
+    if (!TAIL) return;
     for (int i = t; i < a.span / 32; i += NT) bits[i] = 0;
     __syncthreads();
     mark_listed<NT>(a, row, 0, V, bits);
     __syncthreads();
-  }
-  if (wave == NT / 64 - 1) {
+  };
+  constexpr int NS = NT - ASIDE;  // the last wave gathers what is listed
+  auto aside = [&] {
     Known n;
     gather<T, TAIL, TWO>(a, row, l, n);
     if ((t & 63) == 0) known = n;
-  }
-  const float4 sums = sums_of<T, TAIL, TWO, NT>(a, x, 0, V, bits, red);
+  };
+  if (NS == NT && wave == NT / 64 - 1) aside();
+  const float4 sums = sums_of<T, TAIL, TWO, NT, NS>(a, x, 0, V, bits, red, mark, aside);
   if (wave == 0) {
     Terms mine;
     double loss;
@@ -619,9 +650,11 @@ __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
   }
   if (!GRAD) return;
   __syncthreads();
-  write_gradient<T, TWO, NT>(a, x, grad, 0, V, terms);
+  float at_label = 0.f;
+  if (wave == NT / 64 - 1) at_label = listed_grads<TAIL>(a, terms, l);
+  if (NS == NT || wave < NT / 64 - 1) write_gradient<T, TWO, NS>(a, x, grad, 0, V, terms);
   __syncthreads();  // the stream's stores come before the patch's
-  if (wave == 0) patch<T, TAIL>(a, row, 0, a.V, terms, l);
+  if (wave == NT / 64 - 1) patch<T>(a, row, 0, a.V, terms, l, at_label);
 }
 
 }  // namespace
