@@ -101,19 +101,13 @@ struct Sums {
 
 // f(eight logits as loaded, column) over columns [c0, c1) of a row, kAhead
 // loads of a lane in flight.  Every lane makes every turn; f looks at the column.
-#ifndef ASIDE
-#define ASIDE 64
-#endif
 constexpr int kAhead = 2;
 
-// `meanwhile` is called with the first loads on their way.
-template <int NT, typename T, typename F, typename G>
-__device__ __forceinline__ void stream(const T* row, uint32_t c0, uint32_t c1, uint32_t V, F f,
-                                       G meanwhile) {
+template <int NT, typename T, typename F>
+__device__ __forceinline__ void stream(const T* row, uint32_t c0, uint32_t c1, uint32_t V, F f) {
   constexpr uint32_t kStride = NT * 8;
   uint32_t col = c0 + threadIdx.x * 8;
   if (V < 8) {  // a load of eight does not fit
-    meanwhile();
     const int n = (int)V - (int)col;
     f(load8(row + col, n), col, n);
     return;
@@ -121,7 +115,6 @@ __device__ __forceinline__ void stream(const T* row, uint32_t c0, uint32_t c1, u
   Raw8<T> q[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) q[u] = ask8(row, col + u * kStride, c1);
-  meanwhile();
   for (uint32_t base = c0; base < c1; base += kAhead * kStride) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -155,17 +148,13 @@ __device__ __forceinline__ void mark_listed(const Args& a, int64_t row, int64_t 
 // The workgroup's sums over columns [c0, c1) (those without a bit), the same
 // in every lane: the first NS lanes read the logits, the others do `aside`
 // instead.
-template <typename T, bool TAIL, bool TWO, int NT, int NS, typename G, typename H>
+template <typename T, bool TAIL, bool TWO, int NT, int NS, typename G>
 __device__ __forceinline__ float4 sums_of(const Args& a, const T* x, uint32_t c0, uint32_t c1,
-                                          const uint32_t* bits, float (*red)[NT / 64], G meanwhile,
-                                          H aside) {
+                                          const uint32_t* bits, float (*red)[NT / 64], G aside) {
   Sums<TWO> sum;
   const bool streams = NS == NT || __builtin_amdgcn_readfirstlane(threadIdx.x) < NS;
-  if (!streams) {
-    meanwhile();
-    aside();
-  } else {
-  stream<NS>(x, c0, c1, (uint32_t)a.V, [&](const Raw8<T>& r, uint32_t col, int n) {
+  if (!streams) aside();
+  auto add = [&](const Raw8<T>& r, uint32_t col, int n) {
     if (n <= 0) return;
     float v[8];
     widen8(r, v);
@@ -177,8 +166,8 @@ __device__ __forceinline__ float4 sums_of(const Args& a, const T* x, uint32_t c0
         if (skip >> i & 1) v[i] = -INFINITY;
     }
     sum.add(v, a.c);
-  }, meanwhile);
-  }
+  };
+  if (streams) stream<NS>(x, c0, c1, (uint32_t)a.V, add);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float top = wave_max(sum.m);
   sum.scale_to(top, a.c);
@@ -211,15 +200,14 @@ __global__ __launch_bounds__(kThreads) void k_distill_sums(Args a) {
   if (weight_of(a, row) == 0.f) return;  // padding: not read
   const int64_t c0 = (int64_t)part * a.span, c1 = min(a.V, c0 + a.span);
   const T* x = static_cast<const T*>(a.logits) + row * a.sl;
-  auto mark = [&] {
-    if (!TAIL) return;
+  if (TAIL) {
     for (int i = threadIdx.x; i < a.span / 32; i += kThreads) bits[i] = 0;
     __syncthreads();
     mark_listed<kThreads>(a, row, c0, c1, bits);
     __syncthreads();
-  };
-  const float4 o = sums_of<T, TAIL, TWO, kThreads, kThreads>(
-      a, x, (uint32_t)c0, (uint32_t)c1, bits, red, mark, [] {});
+  }
+  const float4 o = sums_of<T, TAIL, TWO, kThreads, kThreads>(a, x, (uint32_t)c0, (uint32_t)c1,
+                                                             bits, red, [] {});
   if (threadIdx.x == 0) a.part[row * a.split + part] = o;
 }
 
@@ -547,7 +535,7 @@ __device__ __forceinline__ void write_gradient(const Args& a, const T* x, T* gra
       v[i] = g;
     }
     store8(grad, col, v, n);
-  }, [] {});
+  });
 }
 
 template <typename T, bool TAIL, bool TWO>
@@ -593,11 +581,13 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(Args a) {
 // flight, 256 KB each, fit in the last level's 256 MB (of 4096 rows of 131072
 // bf16, counters: 0.95 GB fetched and 1.08 GB written).
 //
-// Measured on those, with a tail and labels: 454 us, against 608 for the sums
-// and the gradient in launches of their own and 534 for rows held in 256
-// registers a lane (read once, but a row a compute unit leaves nothing to do
-// while its terms are found).  1024 lanes 454 us, 512 494, 256 598; on 2048
-// rows of 8000 columns 52, 33 and 23 us.
+// Measured on those, with a tail and labels: 444 us (4.8 TB/s of the logits read
+// and the gradient written; the vector unit's exponentials and their arithmetic
+// are 250 us of it), against 608 for the sums and the gradient in launches of
+// their own and 534 for rows held in 256 registers a lane (read once, but a row
+// a compute unit leaves nothing to do while its terms are found).  With every
+// wave reading and the last one gathering besides, 1024 lanes took 454 us, 512
+// 494, 256 598, and on 2048 rows of 8000 columns 52, 33 and 23 us.
 
 template <typename T, bool TAIL, bool TWO, bool GRAD, int NT>
 __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
@@ -623,21 +613,21 @@ __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
   const T* x = static_cast<const T*>(a.logits) + row * a.sl;
   uint32_t* bits = reinterpret_cast<uint32_t*>(lds);
   const Listed l = listed_in(lds + (TAIL ? a.span / 8 : 0), a.K);
-  auto mark = [&] {
-    if (!TAIL) return;
+  if (TAIL) {
     for (int i = t; i < a.span / 32; i += NT) bits[i] = 0;
     __syncthreads();
     mark_listed<NT>(a, row, 0, V, bits);
     __syncthreads();
-  };
-  constexpr int NS = NT - ASIDE;  // the last wave gathers what is listed
+  }
+  // The last wave gathers what is listed while the others read, and finds the
+  // listed ids' gradients while they write.
+  constexpr int NS = NT - 64;
   auto aside = [&] {
     Known n;
     gather<T, TAIL, TWO>(a, row, l, n);
     if ((t & 63) == 0) known = n;
   };
-  if (NS == NT && wave == NT / 64 - 1) aside();
-  const float4 sums = sums_of<T, TAIL, TWO, NT, NS>(a, x, 0, V, bits, red, mark, aside);
+  const float4 sums = sums_of<T, TAIL, TWO, NT, NS>(a, x, 0, V, bits, red, aside);
   if (wave == 0) {
     Terms mine;
     double loss;
@@ -651,8 +641,10 @@ __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
   if (!GRAD) return;
   __syncthreads();
   float at_label = 0.f;
-  if (wave == NT / 64 - 1) at_label = listed_grads<TAIL>(a, terms, l);
-  if (NS == NT || wave < NT / 64 - 1) write_gradient<T, TWO, NS>(a, x, grad, 0, V, terms);
+  if (wave == NT / 64 - 1)
+    at_label = listed_grads<TAIL>(a, terms, l);
+  else
+    write_gradient<T, TWO, NS>(a, x, grad, 0, V, terms);
   __syncthreads();  // the stream's stores come before the patch's
   if (wave == NT / 64 - 1) patch<T>(a, row, 0, a.V, terms, l, at_label);
 }

@@ -9,6 +9,9 @@
 // power of two that covers the row); several teams share a workgroup.  A team
 // walks over rows with the next row's loads in flight, and the parameters stay
 // in its registers.
+//
+// Measured: forward, 8192 x 4096, fp32 residuals and bf16 blocks, layer norms:
+// 72 us, 5.6 TB/s of what it reads and writes once; bound by memory.
 
 #include <algorithm>
 #include <new>
@@ -224,6 +227,11 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_forward(FwdArgs a) {
 //   d_gate = post_weight A + post_bias B,  d_post_weight = sum_g gate A,
 //   d_post_bias = sum_g gate B,
 // so two sums a column serve three outputs.
+//
+// Measured: 32768 x 4096 bf16, rms norms, one gate row: 313 us, 5.1 TB/s over
+// four arrays read and two written, and 8 us for the join; 3001 x 1001 fp16 with
+// a gate a row: 20 and 7.4 us, one round of workgroups whose time is their chain
+// of loads, sums and barriers.
 //
 // Each team sums over rows of its own in registers; a block's teams are added
 // through LDS and one more launch adds the blocks' sums, column by column, in
@@ -873,7 +881,8 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
     full = b->d_post_bias || b->d_pre_bias || gate_bias || p->post == SGB_NORM_LAYER ||
            p->pre == SGB_NORM_LAYER;
     // Two workgroups share a compute unit only where a lane's values fit in 128
-    // registers; else a second would wait for the first to end.
+    // registers; else a second would wait for the first to end (3001 rows of
+    // 1001 fp16 columns with a gate each: 26.4 us in two rounds, 20 in one).
     a.d = deal_rows(p, R, rpg, b->gate != nullptr, true);
     if (full || er == 4 || (b->gate && !a.d.split))
       a.d = deal_rows(p, R, rpg, b->gate != nullptr, false);
