@@ -514,7 +514,7 @@ __device__ __forceinline__ float join_column(const float* p, int64_t parts, int 
                                              float* lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float s = 0.f;
-  constexpr int N = 12;  // loads in flight
+  constexpr int N = 16;  // loads in flight
   for (int64_t k = wave; k < parts; k += 16 * N) {
     float v[N];
 #pragma unroll
