@@ -229,8 +229,8 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_forward(FwdArgs a) {
 // so two sums a column serve three outputs.
 //
 // Measured: 32768 x 4096 bf16, rms norms, one gate row: 313 us, 5.1 TB/s over
-// four arrays read and two written, and 8 us for the join; 3001 x 1001 fp16 with
-// a gate a row: 20 and 7.4 us, one round of workgroups whose time is their chain
+// four arrays read and two written, and 7 us for the join; 3001 x 1001 fp16 with
+// a gate a row: 16 and 5 us, one round of workgroups whose time is their chain
 // of loads, sums and barriers.
 //
 // Each team sums over rows of its own in registers; a block's teams are added
@@ -267,7 +267,7 @@ template <typename T, typename R, int S, bool GROUPED, bool FULL>
 __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   __shared__ float lds[4 * kMaxWaves];
   constexpr int NT = kThreads<S>;
-  __shared__ float fold[S == kWhole ? 1 : NT * 8];
+  __shared__ __attribute__((aligned(16))) float fold[S == kWhole ? 4 : NT * 8 * (FULL ? 4 : 2)];
   const int tpr = a.tpr, D = a.D;
   const int in_block = (int)blockDim.x / tpr;
   const int t = (int)threadIdx.x & (tpr - 1);
@@ -461,28 +461,39 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
       }
   }
   // the block's teams, added in order
-  auto put = [&](int which, float (&s)[8]) {
-    if (!(a.want >> which & 1)) return;
-    float* out = a.par + ((int64_t)which * a.blocks + blockIdx.x) * D;
-      if (S != kWhole && in_block > 1) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fold[i * NT + threadIdx.x] = s[i];
-        __syncthreads();
-        if ((int)threadIdx.x >= tpr) return;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float x = 0.f;
-          for (int m = 0; m < in_block; ++m) x += fold[i * NT + m * tpr + threadIdx.x];
-          s[i] = x;
-        }
-      }
-      store8(out + col, s, n);
-  };
-  put(0, P);
-  if (FULL) put(1, Q);
-  put(2, C);
-  if (FULL) put(3, E);
+  if constexpr (S == kWhole) {
+    float* out = a.par + (int64_t)blockIdx.x * D;
+    const int64_t one = (int64_t)a.blocks * D;
+    if (a.want & 1) store8(out + col, P, n);
+    if (FULL && (a.want & 2)) store8(out + one + col, Q, n);
+    if (a.want & 4) store8(out + 2 * one + col, C, n);
+    if (FULL && (a.want & 8)) store8(out + 3 * one + col, E, n);
+  } else {
+    // One barrier for all of them, and every lane adds: short code, since a
+    // workgroup with few rows waits for it to be fetched.
+    constexpr int kSets = FULL ? 4 : 2;
+    auto leave = [&](int set, const float (&v)[8]) {
+      float4* f = reinterpret_cast<float4*>(fold + (set * NT + (int)threadIdx.x) * 8);
+      f[0] = make_float4(v[0], v[1], v[2], v[3]);
+      f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    leave(0, P);
+    leave(kSets / 2, C);
+    if (FULL) leave(1, Q);
+    if (FULL) leave(3, E);
+    __syncthreads();
+    const int width = tpr * 8, bits = __builtin_ctz(width);
+#pragma unroll 1
+    for (int e = (int)threadIdx.x; e < kSets * width; e += NT) {
+      const int set = e >> bits, c = e & (width - 1);
+      const int which = FULL ? set : 2 * set;
+      if (!(a.want >> which & 1) || c >= D) continue;
+      float x = 0.f;
+#pragma unroll 4
+      for (int m = 0; m < in_block; ++m) x += fold[set * NT * 8 + m * width + c];
+      a.par[((int64_t)which * a.blocks + blockIdx.x) * D + c] = x;
+    }
+  }
 }
 
 // Adds up what the blocks (or a gate's teams) left, column by column: 16
@@ -882,9 +893,9 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
            p->pre == SGB_NORM_LAYER;
     // Two workgroups share a compute unit only where a lane's values fit in 128
     // registers; else a second would wait for the first to end (3001 rows of
-    // 1001 fp16 columns with a gate each: 26.4 us in two rounds, 20 in one).
+    // 1001 fp16 columns with a gate each: 26.4 us in two rounds, 19.7 in one).
     a.d = deal_rows(p, R, rpg, b->gate != nullptr, true);
-    if (full || er == 4 || (b->gate && !a.d.split))
+    if (full || er == 4 || (p->tpr < 64 && b->gate && !a.d.split))
       a.d = deal_rows(p, R, rpg, b->gate != nullptr, false);
     const int64_t per_block = max_threads(p) / p->tpr;
     a.blocks = (int)div_up(a.d.teams, per_block);
