@@ -298,7 +298,9 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   float4 st;
   auto at_row = [&](int64_t row) { return min(row, a.rows - 1); };
   auto at_gate = [&](int64_t g) { return GROUPED ? gate + min(g, a.d.groups - 1) * a.sg : gate; };
-  // without branches, as in the forward; rows past the team's are cleared
+  // without branches, as in the forward; rows past the team's are cleared, their
+  // stats too: they may be another gate's rows, and what is not finite in them
+  // would reach this team's sums through 0 * (1 / deviation)
   auto fetch = [&](int64_t row, int64_t g) {
     const int64_t r = at_row(row);
     st = load_global<float4>((uintptr_t)(a.stats + r * 4));
@@ -311,6 +313,7 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   auto have = [&](int64_t row, int64_t g) {
     const int64_t r = at_row(row);
     const int m = row < r1 ? n : 0;
+    if (row >= r1) st = make_float4(0.f, 0.f, 0.f, 0.f);
     have_row<S>(rdxo, dxo + r * a.sdxo, col, m);
     have_row<S>(rdy, dy ? dy + r * a.sdy : dy, col, m);
     have_row<S>(rx, dy ? x + r * a.sx : (const R*)nullptr, col, m);
@@ -365,8 +368,8 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
     const int64_t row = r0 + k;
     const bool on = row < r1;
     float dyv[8], u[8], v[8], tv[8];
-    const float mh = FULL ? st.x : 0.f, rsh = st.y, mx = FULL ? st.z : 0.f, rsx = st.w;
     have(row, g);
+    const float mh = FULL ? st.x : 0.f, rsh = st.y, mx = FULL ? st.z : 0.f, rsx = st.w;
       widen8(rdxo, tv);
       widen8(rdy, dyv);
       widen8(rx, u);
