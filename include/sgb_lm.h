@@ -30,8 +30,8 @@
  * inputs except where a line here says so.
  *
  * `workspace` is a device buffer, 256-byte aligned, of at least the size that
- * the operator's *_workspace_bytes() gives for that many rows; its contents
- * need no initialisation.  Two calls that may run at the same time need one
+ * the operator's *_workspace_bytes() gives for that many rows or for more; its
+ * contents need no initialisation.  Two calls that may run at the same time need one
  * each.
  */
 #ifndef SGB_LM_H

@@ -671,6 +671,16 @@ int split_of(const sgb_distill_s* p, int64_t rows) {
   return (int)std::max(least, std::min(most, want));
 }
 
+// Parts of `rows` or fewer rows: split_of() falls in steps as rows grow, so that
+// fewer rows can have more parts.  r rows have at most r * ceil(w / r) <= w + r - 1
+// of the w workgroups wanted, and never fewer than `least` a row.
+int64_t most_parts(const sgb_distill_s* p, int64_t rows) {
+  const int64_t most = std::min<int64_t>(kMaxSplit, div_up(p->V, kStep));
+  const int64_t least = div_up(p->V, kMaxSpan);
+  const int64_t wanted = std::min(rows * most, 4 * (int64_t)p->cus + rows);
+  return std::max(rows * least, wanted);
+}
+
 enum What { kLoss, kBackward, kBoth };
 
 template <typename T, bool TAIL, bool TWO, bool GRAD, int NT>
@@ -838,7 +848,7 @@ void sgb_distill_destroy(sgb_distill p) { delete p; }
 
 sgb_status sgb_distill_workspace_bytes(sgb_distill p, int64_t rows, size_t* bytes) {
   if (!p || !bytes || rows < 0 || rows >= (1ll << 25)) return SGB_ERR_INVALID_ARGUMENT;
-  *bytes = kHeaderBytes + align_up((size_t)rows * split_of(p, rows) * sizeof(float4), 256);
+  *bytes = kHeaderBytes + align_up((size_t)most_parts(p, rows) * sizeof(float4), 256);
   return SGB_OK;
 }
 
