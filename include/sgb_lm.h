@@ -155,6 +155,10 @@ sgb_status sgb_block_norm_backward(sgb_block_norm plan, const sgb_norm_params* p
  *      vocabulary)  p_k = exp(v_k / T - lse), the rest p' = max(0, 1 - sum p)
  *      against the student's mass q' outside the listed ids:
  *      KL = sum_k p_k (log p_k - log q[ids_k]) + p' (log p' - log q');
+ *      p' is 0 where every id is listed, and where it is no more than what
+ *      the rounding of an fp32 lse leaves, 2^-20 (1 + |lse|), while every
+ *      logit outside is -inf or 150 T ln 2 below the largest listed (q' below
+ *      2^-126): tokens barred for teacher and student alike;
  *  KL = 0 where nothing is listed.
  *      loss = weight * (kd_weight * T^2 * KL + ce_weight * CE),
  * CE the cross-entropy of softmax(x) at the label (0 for a label < 0).

@@ -213,6 +213,15 @@ __global__ __launch_bounds__(kThreads) void k_distill_sums(Args a) {
 
 // ------------------------------------------------------------- listed terms
 
+// The teacher's tail is 1 - sum p, a difference that the rounding of an fp32
+// teacher_lse leaves above 0 in half of the rows whose listed ids are all the
+// teacher gave mass to.  Against a student mass that is 0 (or so small that its
+// logarithm is a mask's huge number) that rounding would make the loss infinite:
+// up to 16 fp32 roundings of the log-sum-exp count as no tail where the logits
+// outside are 2^-150 of the largest listed or less (2^23 of them 2^-127 of q).
+constexpr float kLseRounding = 0x1p-20f;
+constexpr float kNoMass = -150.f;
+
 // What the row's gradient and loss need, by one wave.
 struct Terms {
   double base;                // the largest logit; logarithms of sums are relative to it (a
@@ -271,8 +280,11 @@ struct Known {
   float top;        // the largest listed logit
   float label_x, w, above;
   int64_t label;    // -1: none
-  int some, repeated;
+  int tail, repeated;
 };
+// Known::tail: none, as nothing or every id of the vocabulary is listed; as it
+// comes; no more than the rounding of teacher_lse
+enum { kNoTail, kTail, kSlightTail };
 
 template <typename T, bool TAIL, bool TWO>
 __device__ __forceinline__ void gather(const Args& a, int64_t row, const Listed& l, Known& o) {
@@ -311,8 +323,15 @@ __device__ __forceinline__ void gather(const Args& a, int64_t row, const Listed&
     l.owner[k] = own;
     l.x[k] = x;
   }
-  o.some = __ballot(some) != 0;
+  const bool any = __ballot(some) != 0;
   o.repeated = __ballot(twice) != 0;
+  o.tail = TAIL && any ? kTail : kNoTail;
+  if (TAIL && a.V <= a.K) {  // can every id be listed?  (Counted apart from the loop above:
+                             // in it, 4096 rows of 131072 took 497 us for 451.)
+    float distinct = 0.f;
+    for (int k = lane; k < a.K; k += 64) distinct += (float)l.owner[k];
+    if (wave_add(distinct) == (float)a.V) o.tail = kNoTail;
+  }
   tmax = wave_max(tmax);
   o.top = wave_max(top);
 
@@ -349,6 +368,8 @@ __device__ __forceinline__ void gather(const Args& a, int64_t row, const Listed&
   o.entropy = wave_add(entropy);
   o.reach = wave_add(reach);
   o.psum = wave_add(psum);
+  if (TAIL && o.tail && (float)(1.0 - o.psum) <= kLseRounding * (1.f + fabsf((float)tl)))
+    o.tail = kSlightTail;
   o.ls = TAIL ? wave_add(ls) : 0.0;
   o.ls1 = TAIL && TWO ? wave_add(ls1) : 0.0;
 
@@ -396,7 +417,8 @@ __device__ __forceinline__ void finish(const Args& a, const Known& n, float4 sum
   o.tail = 0.0;
   o.mass = n.psum == 0.0 ? 0.0 : 1.0;
   if (TAIL) {
-    o.tail = n.some ? fmax(0.0, 1.0 - n.psum) : 0.0;
+    o.tail = n.tail ? fmax(0.0, 1.0 - n.psum) : 0.0;
+    if (n.tail == kSlightTail && (sums.y == 0.f || (sums.x - n.top) * a.c < kNoMass)) o.tail = 0.0;
     o.mass = n.psum + o.tail;
     if (o.tail > 0.0) kl += o.tail * (log(o.tail) - (o.lse_out - o.lse));
   }
