@@ -165,8 +165,8 @@ sgb_status sgb_block_norm_backward(sgb_block_norm plan, const sgb_norm_params* p
  * The gradient is grad_scale * grad_loss * d loss / d x, in the logits' type.
  *
  * A row of weight 0 (padding) is not read: its loss and gradient are 0
- * whatever it holds.  -inf logits have q = 0; a row of nothing else has no
- * distribution and its loss and gradient are NaN.  An id listed twice counts
+ * whatever it holds.  -inf logits have q = 0; any other row of nothing else has
+ * no distribution, and whatever is listed its loss and gradient are NaN.  An id listed twice counts
  * twice in the sums over k and once in q'.
  */
 typedef struct sgb_distill_s* sgb_distill;

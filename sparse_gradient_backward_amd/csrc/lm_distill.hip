@@ -441,6 +441,7 @@ __device__ __forceinline__ void finish(const Args& a, const Known& n, float4 sum
     ca += cb;
     cb = 0.0;
   }
+  if (s == 0.0) loss = ca = o.mass = NAN;  // nothing but -inf: no distribution
   o.ca = (float)ca;
   o.cb = (float)cb;
 }

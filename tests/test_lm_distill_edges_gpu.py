@@ -1,5 +1,6 @@
 """GPU: distillation where a distribution has no mass: every id listed under the
-teacher's true log-sum-exp, masked logits outside what is listed."""
+teacher's true log-sum-exp, rows of nothing but -inf, masked logits outside what
+is listed."""
 import pytest
 import torch
 
@@ -64,6 +65,29 @@ def test_all_listed_and_the_true_log_sum_exp(lm, V, K, dt, T, ce):
             "grad": (grad, half_step(grad, dt) + 256 * U * 2 * (kd * T + ce) * reach[:, None])}
     for l, gr in calls(lm, x, ids, vals, lse, labels, T, kd, ce):
         strict.check({"loss": l, "grad": gr}, want, f"V={V} K={K} {dt} T={T} ce={ce}")
+
+
+@pytest.mark.parametrize("V,rows", [(300, 6), (20011, 6), (20011, 140)])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("T,ce", [(1.0, 0.0), (2.0, 0.3), (1.0, 0.3)])
+def test_rows_of_nothing_but_minus_infinity(lm, V, rows, tail, T, ce):
+    """No distribution: loss and gradient are NaN, whatever is listed; the other
+    rows' are not."""
+    g = torch.Generator().manual_seed(V + rows)
+    x = torch.randn(rows, V, generator=g)
+    teacher = x + torch.randn(rows, V, generator=g)
+    vals, ids = teacher.topk(9, dim=1)
+    lse = torch.logsumexp(teacher.double() / T, 1).float() if tail else None
+    labels = torch.randint(0, V, (rows,), generator=g)
+    x[1] = x[2] = x[4] = -torch.inf
+    ids[2] = ids[3] = -1                # nothing listed: with and without a mass
+    labels[4] = labels[3] = -1
+    none = torch.zeros(rows, dtype=torch.bool)
+    none[[1, 2, 4]] = True
+    for l, gr in calls(lm, x, ids, vals, lse, labels, T, 0.7, ce):
+        assert torch.equal(l.cpu().isnan(), none)
+        assert torch.equal(gr.cpu().isnan(), none[:, None].expand(rows, V))
+        assert float(l[3]) == 0 and not bool(gr[3].any())
 
 
 @pytest.mark.parametrize("V", [300, 20011])
