@@ -48,8 +48,8 @@ extern "C" {
 
 /*
  * sgb_lm_device_status -- synchronises `stream`, then stores in *out the
- * first error the kernels of the last call that used `workspace` recorded
- * (SGB_OK if none; the replays of a captured call count as one call).
+ * first error the kernels of the last call with rows that used `workspace`
+ * recorded (SGB_OK if none; the replays of a captured call count as one call).
  * Distillation and penalties record
  * SGB_ERR_INDEX_OUT_OF_RANGE (an entry, label, token, bias id or mask index
  * at or past its range; it is left out and the rest computed) and

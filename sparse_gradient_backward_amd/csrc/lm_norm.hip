@@ -252,6 +252,8 @@ struct BwdArgs {
   void *dx, *dh, *dgate;
   float* par;   // [4][blocks][D]: sums of t v, t (times the gate unless `raw`), dy u, dy
   float* slot;  // [teams][D] d_gate of a team, where several share a gate
+  Header* hdr;
+  uint32_t epoch;
   int64_t sdxo, sdy, sx, sh, sg, sdx, sdh, sdg;
   int64_t rows, rpg;
   Deal d;
@@ -273,6 +275,8 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   const int t = (int)threadIdx.x & (tpr - 1);
   const int64_t team = (int64_t)blockIdx.x * in_block + team_in_block<S>(tpr);
   const int col = t * 8, n = min(8, D - col);
+  // no error to record, but an earlier call's is no longer the last one's
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->epoch = a.epoch;
   int64_t r0, r1, g0;  // the team's rows; its (first) gate row
   // (rows, teams and gates are below 2^31: 32-bit divisions)
   if (a.d.split) {
@@ -909,6 +913,8 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
     parts = a.d.split && !a.raw && b->d_gate;
     if (kHeaderBytes + (size_t)(4 * a.blocks + (parts ? a.d.teams : 0)) * D * sizeof(float) > need)
       return SGB_ERR_INTERNAL;
+    a.hdr = static_cast<Header*>(ws);
+    a.epoch = next_epoch();
     a.par = reinterpret_cast<float*>(static_cast<char*>(ws) + kHeaderBytes);
     a.slot = parts ? a.par + (int64_t)4 * a.blocks * D : nullptr;
     grouped = !a.d.split && b->gate;
