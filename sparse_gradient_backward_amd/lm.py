@@ -362,6 +362,10 @@ class LogitsPenalty(_Plan):
             if words < (self.vocab + 31) // 32:
                 _bad(w, f"mask must have {(self.vocab + 31) // 32} words a row")
             pm, sm = self._matrix("mask", mask, i32, mask.shape, w)
+            if masks == 0:   # no address, but a set all the same: every index is past its end
+                if mask_index is None and rows:
+                    _bad(w, "mask must have a row for each of the logits' without mask_index")
+                pm = self._vector("mask_index", mask_index, i32, rows, w)
         args = _PENALTY.pack(
             pl, po, pt, self._vector("prompt_lens", prompt_lens, i32, rows, w),
             self._vector("lens", lens, i32, rows, w),
