@@ -350,9 +350,14 @@ class LogitsPenalty(_Plan):
         po, so = self._matrix("out", out, dt, full, w)
         L = n = masks = 0
         pt = st_ = pbi = sbi = pb = sb = pm = sm = 0
+        for name, t in (("tokens", tokens), ("bias_ids", bias_ids), ("mask", mask)):
+            if t is not None and t.dim() != 2:
+                _bad(w, f"{name} must be a matrix")
         if tokens is not None:
             L = tokens.shape[1]
             pt, st_ = self._matrix("tokens", tokens, i32, torch.Size((rows, L)), w)
+        if bias_values is not None and bias_ids is None:
+            _bad(w, "bias_values without bias_ids")
         if bias_ids is not None:
             n = bias_ids.shape[1]
             pbi, sbi = self._matrix("bias_ids", bias_ids, i32, torch.Size((rows, n)), w)

@@ -26,3 +26,15 @@ def test_no_masks_for_rows_that_have_one_each():
     assert status(mask=masks) == "SGB_ERR_INVALID_ARGUMENT"
     assert status(mask=torch.zeros(3, 2, dtype=torch.int32)) == "SGB_ERR_HIP"
     assert status(mask=masks, mask_index=torch.zeros(3, dtype=torch.int32)) == "SGB_ERR_HIP"
+
+
+@no_gpu
+def test_arguments_without_what_they_belong_to():
+    """Dropped in silence, the logits would go without their biases; a mask
+    index alone means nothing, as mask says whether there are masks."""
+    i32 = torch.int32
+    for kw in (dict(bias_values=torch.zeros(3, 2)), dict(tokens=torch.zeros(3, dtype=i32)),
+               dict(bias_ids=torch.zeros(3, dtype=i32)), dict(mask=torch.zeros(2, dtype=i32)),
+               dict(mask=torch.zeros(1, 2, 2, dtype=i32))):
+        assert status(**kw) == "SGB_ERR_INVALID_ARGUMENT", kw
+    assert status(mask_index=torch.zeros(3, dtype=i32)) == "SGB_ERR_HIP"
