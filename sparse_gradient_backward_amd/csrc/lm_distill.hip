@@ -467,7 +467,7 @@ __device__ __forceinline__ float4 join_sums(const Args& a, const float4* part) {
 // The loss alone (and the sums that a backward starts from): a wave a row.
 template <typename T, bool TAIL, bool TWO>
 __global__ __launch_bounds__(64) void k_distill_loss(Args a) {
-  extern __shared__ char lds[];
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int64_t row = blockIdx.x;
   float4* st = reinterpret_cast<float4*>(a.stats);
   if (weight_of(a, row) == 0.f) {
@@ -563,7 +563,7 @@ __device__ __forceinline__ void write_gradient(const Args& a, const T* x, T* gra
 
 template <typename T, bool TAIL, bool TWO>
 __global__ __launch_bounds__(kThreads) void k_distill_grad(Args a) {
-  extern __shared__ char lds[];
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ Terms t;
   const int64_t row = blockIdx.x / (uint32_t)a.split;
   const int part = (int)(blockIdx.x % (uint32_t)a.split);
@@ -614,7 +614,7 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(Args a) {
 
 template <typename T, bool TAIL, bool TWO, bool GRAD, int NT>
 __global__ __launch_bounds__(NT) void k_distill_row(Args a) {
-  extern __shared__ char lds[];
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ Terms terms;
   __shared__ Known known;
   __shared__ float red[3][NT / 64];

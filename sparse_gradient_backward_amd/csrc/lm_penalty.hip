@@ -66,7 +66,7 @@ struct __attribute__((packed, aligned(4))) Int4 {
 
 template <typename T>
 __global__ __launch_bounds__(kMostThreads) void k_penalty(Args a) {
-  extern __shared__ uint32_t word[];  // slice words
+  extern __shared__ __attribute__((aligned(16))) uint32_t word[];  // slice words
   __shared__ int twice;
   const int64_t row = blockIdx.x / a.slices;
   const int64_t v0 = (int64_t)(blockIdx.x % a.slices) * a.slice;
