@@ -26,8 +26,11 @@
  * A matrix argument is a pointer to row 0 and a row stride in elements
  * (>= its width; the elements of a row are adjacent).  Pointers need no more
  * than their element's alignment.  Rows may be 0: nothing is enqueued, and
- * gradient sums over rows are then written as zeros.  Outputs must not overlap
- * inputs except where a line here says so.
+ * gradient sums over rows are then written as zeros; the most are 2^31 - 1 for
+ * block norms, and for the others what one launch of fewer than 2^32 threads
+ * takes (SGB_ERR_UNSUPPORTED past it): 2^24 - 1 rows of up to 32 KB of logits
+ * for distillation, 2^23 - 1 rows of up to 1024 logits for penalties, fewer
+ * the longer.  Outputs must not overlap inputs except where a line here says so.
  *
  * `workspace` is a device buffer, 256-byte aligned, of at least the size that
  * the operator's *_workspace_bytes() gives for that many rows or for more; its

@@ -716,12 +716,16 @@ void run_rows(Args a, hipStream_t s) {
 
 // The longer the row, the more lanes: few rows in flight are long enough to
 // keep the memory busy, and they have to fit in the caches.
+int row_threads(size_t bytes) {
+  return bytes <= kShortRow ? 256 : bytes <= 4 * kShortRow ? 512 : 1024;
+}
+
 template <typename T, bool TAIL, bool TWO, bool GRAD>
 void run_rows(const Args& a, hipStream_t s) {
-  const size_t bytes = (size_t)a.V * sizeof(T);
-  if (bytes <= kShortRow)
+  const int threads = row_threads((size_t)a.V * sizeof(T));
+  if (threads == 256)
     run_rows<T, TAIL, TWO, GRAD, 256>(a, s);
-  else if (bytes <= 4 * kShortRow)
+  else if (threads == 512)
     run_rows<T, TAIL, TWO, GRAD, 512>(a, s);
   else
     run_rows<T, TAIL, TWO, GRAD, 1024>(a, s);
@@ -733,6 +737,13 @@ void run_rows(const Args& a, hipStream_t s) {
 // takes 10.1 and 9.5.)
 bool rows_at_once(const Args& a, size_t elem, int cus) {
   return a.V <= kMaxSpan && (a.rows >= cus / 2 || (size_t)a.V * elem <= kShortRow);
+}
+
+// Threads of the call's largest launch.
+int64_t threads_of(const Args& a, What what, size_t elem, int cus) {
+  return what != kBackward && rows_at_once(a, elem, cus)
+             ? a.rows * row_threads((size_t)a.V * elem)
+             : a.rows * a.split * kThreads;
 }
 
 template <typename T, bool TAIL, bool TWO>
@@ -797,8 +808,6 @@ sgb_status run(sgb_distill p, const sgb_distill_args* q, void* ws, size_t ws_byt
   const sgb_status st = sgb_distill_workspace_bytes(p, R, &need);
   if (st != SGB_OK) return st;
   if (ws_bytes < need) return SGB_ERR_WORKSPACE_TOO_SMALL;
-  DeviceGuard guard(p->device);
-  if (!guard.ok) return SGB_ERR_HIP;
 
   Args a{};
   a.logits = q->logits;
@@ -830,6 +839,9 @@ sgb_status run(sgb_distill p, const sgb_distill_args* q, void* ws, size_t ws_byt
   a.kd = p->kd;
   a.ce = p->ce;
   a.scale = what == kLoss ? 1.f : q->grad_scale;
+  if (threads_of(a, what, e, p->cus) > kMostThreadsAtOnce) return SGB_ERR_UNSUPPORTED;
+  DeviceGuard guard(p->device);
+  if (!guard.ok) return SGB_ERR_HIP;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream_);
   if (q->dtype == SGB_F32)
     run_typed<float>(a, what, p->cus, s);

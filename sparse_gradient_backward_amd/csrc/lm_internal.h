@@ -344,6 +344,9 @@ inline bool matrix_ok(const void* p, int64_t width, int64_t stride, size_t elem)
   return p && aligned(p, elem) && stride >= width && stride <= (1ll << 40);
 }
 
+// A launch of more threads is refused by the runtime.
+constexpr int64_t kMostThreadsAtOnce = (1ll << 32) - 1;
+
 inline bool workspace_ok(const void* ws) { return ws && aligned(ws, 256); }
 
 // Do the bytes of two row-strided matrices (of `rows` rows, or rows_b the

@@ -317,10 +317,11 @@ sgb_status sgb_penalty_apply(sgb_penalty p, const sgb_penalty_args* q, void* ws,
   a.slice = kMinSlice;
   while (a.slice < kMaxSlice && R * div_up(V, a.slice * 2) >= 2 * p->cus) a.slice *= 2;
   a.slices = (int)div_up(V, a.slice);
-  if (R * a.slices >= (1ll << 31)) return SGB_ERR_UNSUPPORTED;
+  const int nt = a.L > kThreads * kAhead * 4 ? kMostThreads : kThreads;
+  if (R * a.slices > kMostThreadsAtOnce / nt) return SGB_ERR_UNSUPPORTED;
   DeviceGuard guard(p->device);
   if (!guard.ok) return SGB_ERR_HIP;
-  const dim3 grid((unsigned)(R * a.slices)), threads(a.L > kThreads * kAhead * 4 ? kMostThreads : kThreads);
+  const dim3 grid((unsigned)(R * a.slices)), threads(nt);
   const size_t lds = (size_t)a.slice * 4;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream_);
   if (q->dtype == SGB_F32)
