@@ -30,7 +30,10 @@
  * block norms, and for the others what one launch of fewer than 2^32 threads
  * takes (SGB_ERR_UNSUPPORTED past it): 2^24 - 1 rows of up to 32 KB of logits
  * for distillation, 2^23 - 1 rows of up to 1024 logits for penalties, fewer
- * the longer.  Outputs must not overlap inputs except where a line here says so.
+ * the longer.  Outputs must not overlap inputs or each other except where a line
+ * here says so.  Refused are overlaps among the matrices of D, V or vocab
+ * columns, and of the parameters' gradients with other outputs; the rest
+ * (stats, losses, lists) is the caller's care.
  *
  * `workspace` is a device buffer, 256-byte aligned, of at least the size that
  * the operator's *_workspace_bytes() gives for that many rows or for more; its

@@ -350,9 +350,9 @@ constexpr int64_t kMostThreadsAtOnce = (1ll << 32) - 1;
 inline bool workspace_ok(const void* ws) { return ws && aligned(ws, 256); }
 
 // Do the bytes of two row-strided matrices (of `rows` rows, or rows_b the
-// second) share a range?  (Interleaved rows
-// of one buffer, e.g. the halves of wider rows, are told apart by `same
-// stride, disjoint columns`.)
+// second) share a range?  (Interleaved rows of one buffer, e.g. the halves of
+// wider rows, are told apart by `same stride, disjoint columns`; the stride of a
+// single row says nothing and is taken for the other's.)
 inline bool overlap(const void* a, int64_t wa, int64_t sa, size_t ea, const void* b, int64_t wb,
                     int64_t sb, size_t eb, int64_t rows, int64_t rows_b = -1) {
   if (rows_b < 0) rows_b = rows;
@@ -361,8 +361,9 @@ inline bool overlap(const void* a, int64_t wa, int64_t sa, size_t ea, const void
   const uint64_t la = ((uint64_t)(rows - 1) * sa + wa) * ea,
                  lb = ((uint64_t)(rows_b - 1) * sb + wb) * eb;
   if (a0 + la <= b0 || b0 + lb <= a0) return false;
-  if (sa * (int64_t)ea != sb * (int64_t)eb || (rows < 2 && rows_b < 2)) return true;
-  const uint64_t pitch = (uint64_t)sa * ea;
+  if (rows < 2 && rows_b < 2) return true;
+  const uint64_t pitch = rows < 2 ? (uint64_t)sb * eb : (uint64_t)sa * ea;
+  if (rows >= 2 && rows_b >= 2 && pitch != (uint64_t)sb * eb) return true;
   const uint64_t d = (b0 >= a0 ? b0 - a0 : pitch - (a0 - b0) % pitch) % pitch;
   // b's columns start d bytes after a's in the shared pitch
   return !(d >= (uint64_t)wa * ea && d + (uint64_t)wb * eb <= pitch);

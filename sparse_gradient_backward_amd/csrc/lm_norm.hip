@@ -862,6 +862,23 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
           return SGB_ERR_INVALID_ARGUMENT;
       }
     const int64_t G = b->gate ? div_up(R, b->rows_per_gate) : 0;
+    // d_gate is written while other gates' rows are still read
+    for (const M& m : in)
+      if (overlap(b->d_gate, D, b->d_gate_stride, e, m.p, D, m.s, m.e, G, R))
+        return SGB_ERR_INVALID_ARGUMENT;
+    // the sums over rows against the other outputs and each other
+    const void* sums[] = {b->d_post_weight, b->d_post_bias, b->d_pre_weight, b->d_pre_bias};
+    for (const M& m : out)
+      if (overlap(b->d_gate, D, b->d_gate_stride, e, m.p, D, m.s, m.e, G, R))
+        return SGB_ERR_INVALID_ARGUMENT;
+    for (int i = 0; i < 4; ++i) {
+      if (overlap(sums[i], D, D, 4, b->d_gate, D, b->d_gate_stride, e, 1, G))
+        return SGB_ERR_INVALID_ARGUMENT;
+      for (const M& m : out)
+        if (overlap(sums[i], D, D, 4, m.p, D, m.s, m.e, 1, R)) return SGB_ERR_INVALID_ARGUMENT;
+      for (int j = 0; j < i; ++j)
+        if (overlap(sums[i], D, D, 4, sums[j], D, D, 4, 1)) return SGB_ERR_INVALID_ARGUMENT;
+    }
     if (overlap(b->dx, D, b->dx_stride, er, b->dh, D, b->dh_stride, e, R) ||
         overlap(b->gate, D, b->gate_stride, e, b->d_gate, D, b->d_gate_stride, e, G) ||
         overlap(b->gate, D, b->gate_stride, e, b->dx, D, b->dx_stride, er, G, R) ||
