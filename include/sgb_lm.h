@@ -25,7 +25,8 @@
  *
  * A matrix argument is a pointer to row 0 and a row stride in elements
  * (>= its width; the elements of a row are adjacent).  Pointers need no more
- * than their element's alignment.  Rows may be 0: nothing is enqueued, and
+ * than their element's alignment, but for stats, four floats a row that are
+ * read at once: 16 bytes, where they are written too.  Rows may be 0: nothing is enqueued, and
  * gradient sums over rows are then written as zeros; the most are 2^31 - 1 for
  * block norms, and for the others what one launch of fewer than 2^32 threads
  * takes (SGB_ERR_UNSUPPORTED past it): 2^24 - 1 rows of up to 32 KB of logits

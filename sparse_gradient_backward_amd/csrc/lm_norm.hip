@@ -766,7 +766,7 @@ sgb_status sgb_block_norm_forward(sgb_block_norm p, const sgb_norm_params* q,
   if (!matrix_ok(f->x, D, f->x_stride, er) || !matrix_ok(f->h, D, f->h_stride, e) ||
       !matrix_ok(f->x_out, D, f->x_out_stride, er) ||
       (f->y && !matrix_ok(f->y, D, f->y_stride, e)) ||
-      (f->gate && !matrix_ok(f->gate, D, f->gate_stride, e)) || !aligned(f->stats, 4))
+      (f->gate && !matrix_ok(f->gate, D, f->gate_stride, e)) || !aligned(f->stats, 16))
     return SGB_ERR_INVALID_ARGUMENT;
   const int64_t G = f->gate ? div_up(R, f->rows_per_gate) : 0;
   const bool x_in_place = f->x_out == f->x && f->x_out_stride == f->x_stride;
