@@ -178,7 +178,7 @@ sgb_status sgb_block_norm_backward(sgb_block_norm plan, const sgb_norm_params* p
  */
 typedef struct sgb_distill_s* sgb_distill;
 
-/* V: 1..2^23; K: 1..1024; T > 0; the weights finite. */
+/* V: 1..2^23; K: 1..1024; T > 0 with log2(e) / T finite in fp32; the weights finite. */
 sgb_status sgb_distill_create(sgb_distill* out, int64_t V, int32_t K, float temperature,
                               float kd_weight, float ce_weight);
 void sgb_distill_destroy(sgb_distill plan);

@@ -859,7 +859,8 @@ extern "C" {
 sgb_status sgb_distill_create(sgb_distill* out, int64_t V, int32_t K, float T, float kd, float ce) {
   if (!out) return SGB_ERR_INVALID_ARGUMENT;
   *out = nullptr;
-  if (V < 1 || K < 1 || K > kMaxK || !(T > 0.f) || !std::isfinite(T) || !std::isfinite(kd) ||
+  if (V < 1 || K < 1 || K > kMaxK || !(T > 0.f) || !std::isfinite(T) ||
+      !std::isfinite((float)(1.4426950408889634074 / (double)T)) || !std::isfinite(kd) ||
       !std::isfinite(ce))
     return SGB_ERR_INVALID_ARGUMENT;
   if (V > kMaxV) return SGB_ERR_UNSUPPORTED;
