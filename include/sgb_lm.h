@@ -220,7 +220,8 @@ sgb_status sgb_distill_loss_grad(sgb_distill plan, const sgb_distill_args* args,
  *  2. generated n > 0 times: x -= frequency * n + presence;
  *  3. x += the sum of the row's biases at v;
  *  4. a mask row is chosen and its bit for v is 0: x = -inf.
- * In fp32, rounded once; a token that none of them touches keeps its bits.
+ * In fp32, rounded once; a token that none of them touches keeps its bits (but a
+ * signalling NaN of 16 bits may come out quiet).
  */
 typedef struct sgb_penalty_s* sgb_penalty;
 

@@ -602,11 +602,16 @@ __global__ __launch_bounds__(kThreads) void k_distill_grad(Args a) {
 // terms and (GRAD) the gradient.  The gradient's reading of the logits comes
 // from the caches: at two workgroups of 1024 lanes a compute unit the rows in
 // flight, 256 KB each, fit in the last level's 256 MB (of 4096 rows of 131072
-// bf16, counters: 0.95 GB fetched and 1.08 GB written).
+// bf16, counters: 0.97 GB fetched and 1.08 GB written).
 //
-// Measured on those, with a tail and labels: 444 us (4.8 TB/s of the logits read
-// and the gradient written; the vector unit's exponentials and their arithmetic
-// are 250 us of it), against 608 for the sums and the gradient in launches of
+// Two share a compute unit at up to 64 registers a lane: so it is but for two
+// sums (T other than 1, and labels), whose forms of 1024 lanes take 68 to 94
+// (only the gradient without a tail 62) and run alone there: 585 us on those rows at
+// T = 2.
+//
+// Measured on those at T = 1, with a tail and labels: 450 us (4.8 TB/s of the
+// logits read and the gradient written; counters: the vector unit is busy for
+// 64% of it), against 608 for the sums and the gradient in launches of
 // their own and 534 for rows held in 256 registers a lane (read once, but a row
 // a compute unit leaves nothing to do while its terms are found).  With every
 // wave reading and the last one gathering besides, 1024 lanes took 454 us, 512
@@ -734,7 +739,10 @@ void run_rows(const Args& a, hipStream_t s) {
 // A row a workgroup, or several workgroups a row and the loss in a launch of
 // its own?  (Loss and gradient: 64 rows of 131072 bf16 take 17 us in parts and
 // 25 as rows, 128 take 26.5 and 26.8, 256 take 43 and 38; of 8000 columns 1 row
-// takes 10.1 and 9.5.)
+// takes 10.1 and 9.5.)  Past kMaxSpan columns a row's bits outgrow the 16 KB set
+// aside for them; what a longer row in one workgroup would take, with or without
+// a tail, was not measured (2048 rows of 131072 bf16 take 242 us as rows, of 151936
+// 114 and 251 in parts).
 bool rows_at_once(const Args& a, size_t elem, int cus) {
   return a.V <= kMaxSpan && (a.rows >= cus / 2 || (size_t)a.V * elem <= kShortRow);
 }

@@ -11,7 +11,8 @@
 // in its registers.
 //
 // Measured: forward, 8192 x 4096, fp32 residuals and bf16 blocks, layer norms:
-// 72 us, 5.6 TB/s of what it reads and writes once; bound by memory.
+// 83 us a pass, 4.9 TB/s of what it reads and writes once (72 us where the pass
+// before left part of the inputs in the last-level cache); bound by memory.
 
 #include <algorithm>
 #include <new>
@@ -228,10 +229,11 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_forward(FwdArgs a) {
 //   d_post_bias = sum_g gate B,
 // so two sums a column serve three outputs.
 //
-// Measured: 32768 x 4096 bf16, rms norms, one gate row: 313 us, 5.1 TB/s over
-// four arrays read and two written, and 7 us for the join; 3001 x 1001 fp16 with
-// a gate a row: 16 and 5 us, one round of workgroups whose time is their chain
-// of loads, sums and barriers.
+// Measured: 32768 x 4096 bf16, rms norms, one gate row: 315 us, 5.1 TB/s over
+// four arrays read and two written, and 6 us for the join, and 500 us (4.8 TB/s)
+// with fp32 residuals; 3001 x 1001 fp16 with a gate a row: 17 and 5 us, one round
+// of workgroups whose time is their chain of loads, sums and barriers;
+// 8192 x 4096 bf16, layer norms with biases, a gate for 1024 rows: 79 and 9 us.
 //
 // Each team sums over rows of its own in registers; a block's teams are added
 // through LDS and one more launch adds the blocks' sums, column by column, in
@@ -342,7 +344,10 @@ __global__ __launch_bounds__(kThreads<S>) void k_norm_backward(BwdArgs a) {
   have8_as<TINY>(rqw, a.p.pre_w, pt, col, n, 1.f, qw);
   // A workgroup of 16 waves has 128 registers a lane: the parameters wait in
   // LDS there, each lane's own columns, and are read back where they are used
-  // (in registers they cost over a hundred spills a lane).
+  // (in registers they cost over a hundred spills a lane).  That does not spare
+  // all of them: GROUPED and FULL still spill 20 to 70 registers, two more forms
+  // of fp32 elements 12 and 20; the others none.  8192 x 8192 bf16, layer norms
+  // with biases, a gate a row: 435 us, 1.8 TB/s.
   constexpr bool IN_LDS = S == kWhole;
   __shared__ float4 held[IN_LDS ? 4 * 2 * NT : 1];
   auto put_by = [&](int which, const float (&v)[8]) {
@@ -918,6 +923,12 @@ sgb_status sgb_block_norm_backward(sgb_block_norm p, const sgb_norm_params* q,
     // Two workgroups share a compute unit only where a lane's values fit in 128
     // registers; else a second would wait for the first to end (3001 rows of
     // 1001 fp16 columns with a gate each: 26.4 us in two rounds, 19.7 in one).
+    // 16-bit rms norms fit (two and one: 65536 x 1024 without a gate 153 and 161 us,
+    // 32768 x 4096 with a gate each 380 and 419, with one or none 319 and 304), but
+    // in teams narrower than a wave with gates they take 134.  fp32 residuals need
+    // up to 160; with 16-bit blocks one form, ungrouped teams of waves, takes 127,
+    // and two gain nothing there (3001 x 1024: 18.7 us and 16.1 as one; 32768 x 4096:
+    // 507 to 510 and 452 to 498).
     a.d = deal_rows(p, R, rpg, b->gate != nullptr, true);
     if (full || er == 4 || (p->tpr < 64 && b->gate && !a.d.split))
       a.d = deal_rows(p, R, rpg, b->gate != nullptr, false);

@@ -8,11 +8,12 @@
 // passes as long as the logits.  The logits are loaded into registers before
 // the counting, so that they arrive meanwhile.
 //
-// Measured: 512 rows of 131072 fp32 with 8192 tokens in 101 us, 5.4 TB/s of the
-// logits and tokens read and the logits written, bound by memory; 64 rows of
-// bf16 with 4096 tokens 11.1 us, 9 rows of 50021 fp16 with 60001 tokens 12 us, both one round of
-// workgroups whose time is the chain of loads, counting and streaming and the
-// fetching of their code; one row of 32000 4.3 us, little over an empty launch.
+// Measured: 512 rows of 131072 fp32 with 8192 tokens in 105 us a pass, 5.2 TB/s of
+// the logits and tokens read and the logits written, bound by memory; 64 rows of
+// bf16 with 4096 tokens 10.6 us, 9 rows of 50021 fp16 with 60001 tokens 13 to 15 us,
+// both one round of workgroups whose time is the chain of loads, counting and
+// streaming and the fetching of their code; one row of 32000 4.4 us in the
+// kernel, little over an empty launch.
 
 #include <algorithm>
 #include <cmath>
