@@ -23,23 +23,23 @@
  * SGB_ERR_HIP.  Results do not
  * depend on timing: no floating-point atomics.
  *
- * A matrix argument is a pointer to row 0 and a row stride in elements
- * (>= its width; the elements of a row are adjacent).  Pointers need no more
- * than their element's alignment, but for stats, four floats a row that are
- * read at once: 16 bytes, where they are written too.  Rows may be 0: nothing is enqueued, and
- * gradient sums over rows are then written as zeros; the most are 2^31 - 1 for
- * block norms, and for the others what one launch of fewer than 2^32 threads
- * takes (SGB_ERR_UNSUPPORTED past it): 2^24 - 1 rows of up to 32 KB of logits
- * for distillation, 2^23 - 1 rows of up to 1024 logits for penalties, fewer
- * the longer.  Outputs must not overlap inputs or each other except where a line
- * here says so.  Refused are overlaps among the matrices of D, V or vocab
- * columns, and of the parameters' gradients with other outputs; the rest
+ * A matrix argument is a pointer to row 0 and a row stride in elements (>= its
+ * width; the elements of a row are adjacent).  Pointers need no more than their
+ * element's alignment, but for stats, four floats a row that are read at once:
+ * 16 bytes, where they are written too.  Rows may be 0: nothing is enqueued,
+ * and gradient sums over rows are then written as zeros; the most are 2^31 - 1
+ * for block norms, and for the others what one launch of fewer than 2^32
+ * threads takes (SGB_ERR_UNSUPPORTED past it): 2^24 - 1 rows of up to 32 KB of
+ * logits for distillation, 2^23 - 1 rows of up to 1024 logits for penalties,
+ * fewer the longer.  Outputs must not overlap inputs or each other except where
+ * a line here says so.  Refused are overlaps among the matrices of D, V or
+ * vocab columns, and of the parameters' gradients with other outputs; the rest
  * (stats, losses, lists) is the caller's care.
  *
  * `workspace` is a device buffer, 256-byte aligned, of at least the size that
  * the operator's *_workspace_bytes() gives for that many rows or for more; its
- * contents need no initialisation.  Two calls that may run at the same time need one
- * each.
+ * contents need no initialisation.  Two calls that may run at the same time
+ * need one each.
  */
 #ifndef SGB_LM_H
 #define SGB_LM_H
@@ -171,10 +171,10 @@ sgb_status sgb_block_norm_backward(sgb_block_norm plan, const sgb_norm_params* p
  * CE the cross-entropy of softmax(x) at the label (0 for a label < 0).
  * The gradient is grad_scale * grad_loss * d loss / d x, in the logits' type.
  *
- * A row of weight 0 (padding) is not read: its loss and gradient are 0
- * whatever it holds.  -inf logits have q = 0; any other row of nothing else has
- * no distribution, and whatever is listed its loss and gradient are NaN.  An id listed twice counts
- * twice in the sums over k and once in q'.
+ * A row of weight 0 (padding) is not read: its loss and gradient are 0 whatever
+ * it holds.  -inf logits have q = 0; any other row of nothing else has no
+ * distribution, and whatever is listed its loss and gradient are NaN.  An id
+ * listed twice counts twice in the sums over k and once in q'.
  */
 typedef struct sgb_distill_s* sgb_distill;
 
