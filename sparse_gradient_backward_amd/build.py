@@ -23,6 +23,7 @@ ATOMIC_SOURCES = [os.path.join(CSRC, "atomic_scatter.hip")]
 # the token-model operators
 LM_LIB = os.path.join(HERE, "libsgb_lm.so")
 LM_SOURCES = [os.path.join(CSRC, n) for n in ("lm_norm.hip", "lm_distill.hip", "lm_penalty.hip",
+                                              "lm_vocab_ce.hip", "lm_dropout.hip", "lm_quant.hip",
                                               "lm_api.cpp")]
 ARCH = os.environ.get("SGB_OFFLOAD_ARCH", "gfx950")
 

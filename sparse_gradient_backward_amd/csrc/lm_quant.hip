@@ -1,0 +1,286 @@
+// lm_quant.hip -- root-mean-square norm with the residual's addition and an
+// output in 8 bits with scales, of libsgb_lm.so (definition:
+// include/sgb_lm_step.h).
+//
+// A row is held by a team of lanes, eight columns a lane: the residual sum,
+// its squares' sum, the largest magnitude and the codes come from registers,
+// so each input is read once and each output written once.  A row's scale
+// needs a second fold over the team (largest magnitudes, after the squares); a
+// group's scale only one among the group's neighbouring lanes.
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "lm_internal.h"
+#include "sgb_lm_step.h"
+
+using namespace sgb_lm;
+
+namespace {
+
+constexpr int kMaxCols = 8192;
+constexpr int kMaxWaves = 16;
+
+struct Args {
+  const void *h, *x;
+  void* x_out;
+  const void* weight;
+  uint8_t* q;
+  float* scales;
+  float* stats;
+  int64_t sh, sx, sxo, sq, ss;
+  int64_t rows;
+  int D, tpr, in_group;  // lanes a row, lanes a group
+  int weight_dtype;
+  float eps, inv_d;
+};
+
+// Largest of x over groups of `width` lanes (4, 8, .. 64): one that is no number
+// wins.  Magnitudes as words compare like their values, and NaN above all.
+__device__ __forceinline__ uint32_t fold_most(uint32_t x, int width) {
+  const auto f = [](float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+  };
+  float v = __uint_as_float(x);
+  if (width == 4) {
+    v = f(v, dpp<0xB1>(v));
+    v = f(v, dpp<0x4E>(v));
+  } else {
+    v = wave_fold(v, width, f);
+  }
+  return __float_as_uint(v);
+}
+
+// WAVES: a row is a wave's or less (0), or whole waves' (their number).
+template <typename T, typename U, int CODE, bool WIDE, bool TINY>
+__global__ __launch_bounds__(WIDE ? 1024 : 256) void k_quant(Args a) {
+  __shared__ float sums[2][kMaxWaves];
+  __shared__ uint32_t mosts[2][kMaxWaves];
+  constexpr float kMost = CODE == SGB_CODE_INT8 ? 127.f : 448.f;
+  const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int teams = (int)blockDim.x / a.tpr, nw = WIDE ? a.tpr >> 6 : 1;
+  const int team = WIDE ? __builtin_amdgcn_readfirstlane(t / a.tpr) : t / a.tpr;
+  const int col = (t % a.tpr) * 8, n = max(0, min(8, a.D - col));
+  const int first = wave / nw * nw;
+
+  RawAs wr = ask8_as<TINY>(a.weight, a.weight_dtype, col, a.D);
+  float w[8];
+  have8_as<TINY>(wr, a.weight, a.weight_dtype, col, n, 1.f, w);
+
+  const int64_t step = (int64_t)gridDim.x * teams;
+  int64_t r = (int64_t)blockIdx.x * teams + team;
+  Raw8<T> h;
+  Raw8<U> x;
+  const auto ask = [&](int64_t row) {
+    const int64_t at = min(row, a.rows - 1);  // past the last: loaded, not used
+    if (TINY) {
+      h = load8(static_cast<const T*>(a.h) + at * a.sh + col, n);
+      x = load8(static_cast<const U*>(a.x) + at * a.sx + col, a.x ? n : 0);
+    } else {
+      h = ask8(static_cast<const T*>(a.h) + at * a.sh, (uint32_t)col, (uint32_t)a.D);
+      x = ask8(a.x ? static_cast<const U*>(a.x) + at * a.sx : nullptr, (uint32_t)col, (uint32_t)a.D);
+    }
+  };
+  ask(r);
+  int phase = 0;
+  // every team of a workgroup takes as many turns: barriers are the workgroup's
+  const int64_t turns = (a.rows + step - 1) / step;
+  for (int64_t turn = 0; turn < turns; ++turn, r += step) {
+    const bool mine = r < a.rows;
+    if (!TINY) {
+      have8(h, n);
+      have8(x, n);
+    }
+    float v[8], y[8];
+    widen8(h, v);
+    widen8(x, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += y[i];
+    if (turn + 1 < turns) ask(r + step);
+    if (mine && a.x_out && n > 0) store8(static_cast<U*>(a.x_out) + r * a.sxo + col, v, n);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);  // columns past the row are zeros
+    s = wave_add(s, WIDE ? 64 : a.tpr);
+    if (WIDE) {
+      if (lane == 0) sums[phase][wave] = s;
+      __syncthreads();
+      s = wave_add(lane < nw ? sums[phase][first + lane] : 0.f, 16);
+      s = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(s)));
+    }
+    const float rs = 1.0f / sqrtf(fmaf(s, a.inv_d, a.eps));
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = i < n ? v[i] * rs * w[i] : 0.f;
+      most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+    if (a.in_group) {
+      most = fold_most(most, a.in_group);
+    } else {
+      most = fold_most(most, WIDE ? 64 : a.tpr);
+      if (WIDE) {
+        if (lane == 0) mosts[phase][wave] = most;
+        __syncthreads();
+        most = fold_most(lane < nw ? mosts[phase][first + lane] : 0u, 16);
+        most = (uint32_t)__builtin_amdgcn_readfirstlane((int)most);
+      }
+    }
+    phase ^= 1;
+    float scale = __uint_as_float(most) / kMost;
+    if (scale < 0x1p-126f) scale = 0.f;
+    // A quotient of the rounded scale, each correctly rounded: a product with a
+    // reciprocal moves codes on the border between two.
+    const bool fine = scale > 0.f && scale < INFINITY;  // nor NaN
+    float c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      c[i] = fine ? fminf(fmaxf(v[i] / scale, -kMost), kMost) : 0.f;
+    if (!mine || n <= 0) continue;
+    const int lanes = a.in_group ? a.in_group : a.tpr;
+    const int in_row = t % a.tpr;
+    if (in_row % lanes == 0) a.scales[r * a.ss + in_row / lanes] = scale;
+    if (a.stats && in_row == 0) {
+      typedef float F4 __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<F4*>(a.stats + 4 * r) = F4{0.f, 1.f, 0.f, rs};
+    }
+    uint32_t b[2] = {0, 0};
+    if (CODE == SGB_CODE_INT8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        b[i >> 2] |= ((uint32_t)(int)rintf(c[i]) & 0xffu) << (8 * (i & 3));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int p = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i], c[4 * i + 1], 0, false);
+        b[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i + 2], c[4 * i + 3], p, true);
+      }
+    }
+    uint8_t* out = a.q + r * a.sq + col;
+    if (n >= 8) {
+      typedef uint32_t W2 __attribute__((ext_vector_type(2)));
+      typedef W2 Any __attribute__((aligned(1)));
+      store_global<Any>(out, 0, W2{b[0], b[1]});
+    } else {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n) out[i] = (uint8_t)(b[i >> 2] >> (8 * (i & 3)));
+    }
+  }
+}
+
+template <typename T, typename U, int CODE>
+void launch(const Args& a, unsigned grid, int threads, hipStream_t s) {
+  const dim3 g(grid), b(threads);
+  if (a.D < 8)
+    hipLaunchKernelGGL((k_quant<T, U, CODE, false, true>), g, b, 0, s, a);
+  else if (a.tpr > 64)
+    hipLaunchKernelGGL((k_quant<T, U, CODE, true, false>), g, b, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_quant<T, U, CODE, false, false>), g, b, 0, s, a);
+}
+
+template <typename T, typename U>
+void launch(const Args& a, int code, unsigned grid, int threads, hipStream_t s) {
+  if (code == SGB_CODE_INT8)
+    launch<T, U, SGB_CODE_INT8>(a, grid, threads, s);
+  else
+    launch<T, U, SGB_CODE_E4M3>(a, grid, threads, s);
+}
+
+}  // namespace
+
+struct sgb_quant_norm_s {
+  int device, cus;
+  int D, code, group;
+  float eps;
+};
+
+extern "C" {
+
+sgb_status sgb_quant_norm_create(sgb_quant_norm* out, int32_t D, int32_t code, int32_t group,
+                                 float eps) {
+  if (!out) return SGB_ERR_INVALID_ARGUMENT;
+  *out = nullptr;
+  if (D < 1 || D > kMaxCols || (code != SGB_CODE_INT8 && code != SGB_CODE_E4M3) ||
+      (group != 0 && group != 32 && group != 64 && group != 128 && group != 256 && group != 512) ||
+      !(eps >= 0.f) || std::isinf(eps))
+    return SGB_ERR_INVALID_ARGUMENT;
+  sgb_quant_norm_s* p = new (std::nothrow) sgb_quant_norm_s();
+  if (!p) return SGB_ERR_HIP;
+  p->device = current_device();
+  p->cus = compute_units(p->device);
+  p->D = D;
+  p->code = code;
+  p->group = group;
+  p->eps = eps;
+  *out = p;
+  return SGB_OK;
+}
+
+void sgb_quant_norm_destroy(sgb_quant_norm p) { delete p; }
+
+sgb_status sgb_quant_norm_forward(sgb_quant_norm p, const sgb_quant_norm_args* q, void* stream_) {
+  if (!p || !q) return SGB_ERR_INVALID_ARGUMENT;
+  const int64_t R = q->rows, D = p->D, groups = p->group ? div_up(D, p->group) : 1;
+  if (!float_dtype(q->dtype) || !float_dtype(q->weight_dtype) || R < 0 || R >= (1ll << 31) ||
+      (q->res_dtype != q->dtype && q->res_dtype != SGB_F32) || q->reserved != 0)
+    return SGB_ERR_INVALID_ARGUMENT;
+  if (R == 0) return SGB_OK;
+  const size_t e = elem_size(q->dtype), er = elem_size(q->res_dtype);
+  if (!matrix_ok(q->h, D, q->h_stride, e) || (q->x && !matrix_ok(q->x, D, q->x_stride, er)) ||
+      (q->x_out && !matrix_ok(q->x_out, D, q->x_out_stride, er)) ||
+      !matrix_ok(q->q, D, q->q_stride, 1) || !matrix_ok(q->scales, groups, q->scales_stride, 4) ||
+      !q->weight || !aligned(q->weight, elem_size(q->weight_dtype)) || !aligned(q->stats, 16))
+    return SGB_ERR_INVALID_ARGUMENT;
+  const bool on_x = q->x_out == q->x && (R < 2 || q->x_out_stride == q->x_stride);
+  const bool on_h = q->x_out == q->h && q->res_dtype == q->dtype &&
+                    (R < 2 || q->x_out_stride == q->h_stride);
+  if ((!on_x && overlap(q->x_out, D, q->x_out_stride, er, q->x, D, q->x_stride, er, R)) ||
+      (!on_h && overlap(q->x_out, D, q->x_out_stride, er, q->h, D, q->h_stride, e, R)) ||
+      overlap(q->q, D, q->q_stride, 1, q->h, D, q->h_stride, e, R) ||
+      overlap(q->q, D, q->q_stride, 1, q->x, D, q->x_stride, er, R) ||
+      overlap(q->q, D, q->q_stride, 1, q->x_out, D, q->x_out_stride, er, R))
+    return SGB_ERR_INVALID_ARGUMENT;
+
+  Args a{};
+  a.h = q->h;
+  a.x = q->x;
+  a.x_out = q->x_out;
+  a.weight = q->weight;
+  a.q = q->q;
+  a.scales = q->scales;
+  a.stats = q->stats;
+  a.sh = q->h_stride;
+  a.sx = q->x_stride;
+  a.sxo = q->x_out_stride;
+  a.sq = q->q_stride;
+  a.ss = q->scales_stride;
+  a.rows = R;
+  a.D = (int)D;
+  a.weight_dtype = q->weight_dtype;
+  a.eps = p->eps;
+  a.inv_d = 1.f / (float)D;
+  a.in_group = p->group < D ? p->group / 8 : 0;  // one group: the row's team may be narrower
+  a.tpr = 8;
+  while (a.tpr * 8 < D) a.tpr *= 2;
+  DeviceGuard guard(p->device);
+  if (!guard.ok) return SGB_ERR_HIP;
+  const int threads = a.tpr > 256 ? a.tpr : 256;
+  const int64_t rows_a_block = threads / a.tpr;
+  const int64_t most = (int64_t)p->cus * (2048 / threads);
+  const unsigned grid = (unsigned)std::min(div_up(R, rows_a_block), most);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream_);
+  if (q->dtype == SGB_F32)
+    launch<float, float>(a, p->code, grid, threads, s);
+  else if (q->dtype == SGB_BF16)
+    q->res_dtype == SGB_F32 ? launch<bf16_t, float>(a, p->code, grid, threads, s)
+                            : launch<bf16_t, bf16_t>(a, p->code, grid, threads, s);
+  else
+    q->res_dtype == SGB_F32 ? launch<f16_t, float>(a, p->code, grid, threads, s)
+                            : launch<f16_t, f16_t>(a, p->code, grid, threads, s);
+  return hipGetLastError() == hipSuccess ? SGB_OK : SGB_ERR_HIP;
+}
+
+}  // extern "C"

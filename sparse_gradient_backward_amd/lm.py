@@ -1,6 +1,7 @@
 """Python binding of libsgb_lm.so, the token-model operators (C ABI:
-``include/sgb_lm.h``): block norms, distillation from a teacher's top logits,
-logits penalties.
+``include/sgb_lm.h`` and ``include/sgb_lm_step.h``): block norms, distillation
+from a teacher's top logits, logits penalties; vocabulary cross-entropy,
+dropout, quantising norms.
 
 Argument marshalling only: the computation runs in the library's HIP kernels.
 Every tensor is a device tensor on the plan's GPU; matrices are 2-D with
@@ -14,6 +15,10 @@ this module fails loudly (ImportError) when the library has not been built.
     norm.forward(x, h, x_out, y, gate=gate, rows_per_gate=1024, stats=stats)
     norm.backward(dx_out, dy, x_out, h, stats, dx, dh, gate=gate, rows_per_gate=1024,
                   d_gate=dg, d_post_weight=dw1, d_pre_weight=dw2, workspace=ws)
+
+    head = lm.VocabCrossEntropy(4096, 131072)
+    head.loss_grad(y, table, labels, loss, d_y, d_table, grad_scale=1 / tokens,
+                   workspace=head.workspace(tokens, torch.bfloat16))
 """
 from __future__ import annotations
 
@@ -29,6 +34,7 @@ from . import (DTYPE, SGB_ERR_INVALID_ARGUMENT, SgbError, _check, sgb_status_str
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("SGB_LM_LIBRARY") or os.path.join(_HERE, "libsgb_lm.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "sgb_lm.h")
+STEP_HEADER = os.path.join(os.path.dirname(_HERE), "include", "sgb_lm_step.h")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -54,14 +60,27 @@ for _name, _args in {
         "sgb_penalty_create": [_out, _i64],
         "sgb_penalty_destroy": [_vp],
         "sgb_penalty_workspace_bytes": [_vp, _i64, ctypes.POINTER(_sz)],
-        "sgb_penalty_apply": [_vp, ctypes.c_char_p, _vp, _sz, _vp]}.items():
+        "sgb_penalty_apply": [_vp, ctypes.c_char_p, _vp, _sz, _vp],
+        "sgb_vocab_ce_create": [_out, _i32, _i64],
+        "sgb_vocab_ce_destroy": [_vp],
+        "sgb_vocab_ce_workspace_bytes": [_vp, _i64, _i32, _i32, ctypes.POINTER(_sz)],
+        "sgb_vocab_ce_forward": [_vp, ctypes.c_char_p, _vp, _sz, _vp],
+        "sgb_vocab_ce_backward": [_vp, ctypes.c_char_p, _vp, _sz, _vp],
+        "sgb_vocab_ce_loss_grad": [_vp, ctypes.c_char_p, _vp, _sz, _vp],
+        "sgb_dropout_create": [_out, ctypes.c_double],
+        "sgb_dropout_destroy": [_vp],
+        "sgb_dropout_apply": [_vp, ctypes.c_char_p, _vp],
+        "sgb_quant_norm_create": [_out, _i32, _i32, _i32, _f32],
+        "sgb_quant_norm_destroy": [_vp],
+        "sgb_quant_norm_forward": [_vp, ctypes.c_char_p, _vp]}.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = None if _name.endswith("_destroy") else ctypes.c_int
 
 NORM = {"none": 0, "rms": 1, "layer": 2}
+CODE = {"int8": (0, torch.int8), "fp8": (1, torch.float8_e4m3fn)}
 _DTYPE = {torch.float32: DTYPE["f32"], torch.bfloat16: DTYPE["bf16"], torch.float16: DTYPE["f16"]}
 
-# The argument structs of sgb_lm.h, packed in C layout.  (A call on one token
+# The argument structs of the headers, packed in C layout.  (A call on one token
 # takes a few microseconds in all: a ctypes.Structure would cost more than its
 # kernel.)
 _NORM_PARAMS = struct.Struct("@4Pi4x")
@@ -69,11 +88,14 @@ _NORM_FORWARD = struct.Struct("@6P7q2i")
 _NORM_BACKWARD = struct.Struct("@13P10q2i")
 _DISTILL = struct.Struct("@10P5qif")
 _PENALTY = struct.Struct("@12P7q4i")
+_VOCAB_CE = struct.Struct("@9P5q3if")
+_DROPOUT = struct.Struct("@4P5q2Q4i")
+_QUANT_NORM = struct.Struct("@7P6q4i")
 
 
-def header_functions() -> list:
-    """Names of the functions include/sgb_lm.h declares."""
-    text = open(HEADER).read()
+def header_functions(header: str = HEADER) -> list:
+    """Names of the functions that include/sgb_lm.h (or another header) declares."""
+    text = open(header).read()
     return sorted(set(re.findall(r"^\s*(?:const\s+)?\w+\*?\s+\**(sgb_\w+)\s*\(", text, re.M)))
 
 
@@ -94,7 +116,15 @@ def _stream(stream, index) -> int:
     return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
 
 
-class _Plan:
+def _int(name, v, lo, hi, where) -> int:
+    """An integer that the C struct's field holds."""
+    v = int(v)
+    if not lo <= v < hi:
+        _bad(where, f"{name} must be in [{lo}, {hi})")
+    return v
+
+
+class _Handle:
     """Owns a plan handle of the C library, on the device current at creation."""
     _kind = ""
 
@@ -107,23 +137,6 @@ class _Plan:
         self._device = torch.device("cuda", torch.cuda.current_device()) \
             if torch.cuda.is_available() else torch.device("cpu")
         self._index = -1 if self._device.type == "cpu" else self._device.index
-
-    def workspace_bytes(self, rows: int) -> int:
-        n = _sz()
-        name = f"sgb_{self._kind}_workspace_bytes"
-        _check(getattr(_lib, name)(self.handle, int(rows), ctypes.byref(n)), name)
-        return int(n.value)
-
-    def workspace(self, rows: int) -> torch.Tensor:
-        """A workspace for calls of up to `rows` rows that follow one another."""
-        return torch.empty(self.workspace_bytes(rows), dtype=torch.uint8, device=self._device)
-
-    def device_status(self, workspace, stream=None) -> str:
-        """Waits for `stream`; the first error that the last call on `workspace` recorded."""
-        out = _i32()
-        _check(_lib.sgb_lm_device_status(workspace.data_ptr(), _stream(stream, self._index),
-                                         ctypes.byref(out)), "sgb_lm_device_status")
-        return sgb_status_string(out.value)
 
     def _matrix(self, name, t, dtype, shape, where):
         """Pointer and row stride of a 2-D argument (None: 0, 0)."""
@@ -148,13 +161,6 @@ class _Plan:
             _bad(where, f"{name} must be on {self._device}")
         return t.data_ptr()
 
-    def _space(self, ws, where):
-        if ws is None:
-            _bad(where, "workspace is missing")
-        if ws.get_device() != self._index or not ws.is_contiguous():
-            _bad(where, f"workspace must be contiguous on {self._device}")
-        return ws.data_ptr(), ws.numel() * ws.element_size()
-
     def close(self):
         if getattr(self, "handle", None):
             getattr(_lib, f"sgb_{self._kind}_destroy")(self.handle)
@@ -165,6 +171,34 @@ class _Plan:
             self.close()
         except Exception:
             pass
+
+
+class _Plan(_Handle):
+    """A plan whose calls work in a workspace."""
+
+    def workspace_bytes(self, rows: int) -> int:
+        n = _sz()
+        name = f"sgb_{self._kind}_workspace_bytes"
+        _check(getattr(_lib, name)(self.handle, int(rows), ctypes.byref(n)), name)
+        return int(n.value)
+
+    def workspace(self, rows: int) -> torch.Tensor:
+        """A workspace for calls of up to `rows` rows that follow one another."""
+        return torch.empty(self.workspace_bytes(rows), dtype=torch.uint8, device=self._device)
+
+    def device_status(self, workspace, stream=None) -> str:
+        """Waits for `stream`; the first error that the last call on `workspace` recorded."""
+        out = _i32()
+        _check(_lib.sgb_lm_device_status(workspace.data_ptr(), _stream(stream, self._index),
+                                         ctypes.byref(out)), "sgb_lm_device_status")
+        return sgb_status_string(out.value)
+
+    def _space(self, ws, where):
+        if ws is None:
+            _bad(where, "workspace is missing")
+        if ws.get_device() != self._index or not ws.is_contiguous():
+            _bad(where, f"workspace must be contiguous on {self._device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 class BlockNorm(_Plan):
@@ -382,3 +416,160 @@ class LogitsPenalty(_Plan):
         ws, ws_bytes = self._space(workspace, w)
         _check(_lib.sgb_penalty_apply(self.handle, args, ws, ws_bytes,
                                       _stream(stream, self._index)), w)
+
+
+class VocabCrossEntropy(_Plan):
+    """Cross-entropy of the head's product hidden @ weight.T over a vocabulary
+    of V tokens, D columns, with its gradients, without a matrix of logits."""
+    _kind = "vocab_ce"
+
+    def __init__(self, D: int, V: int):
+        self.D = _int("D", D, -2**31, 2**31, "VocabCrossEntropy")
+        self.V = _int("V", V, -2**63, 2**63, "VocabCrossEntropy")
+        self._create(self.D, self.V)
+
+    def workspace_bytes(self, rows: int, dtype=torch.bfloat16, gradient: bool = True) -> int:
+        w = "sgb_vocab_ce_workspace_bytes"
+        if dtype not in _DTYPE:
+            _bad(w, "dtype must be float32, bfloat16 or float16")
+        n = _sz()
+        _check(_lib.sgb_vocab_ce_workspace_bytes(self.handle, _int("rows", rows, -2**63, 2**63, w),
+                                                 _DTYPE[dtype], int(bool(gradient)),
+                                                 ctypes.byref(n)), w)
+        return int(n.value)
+
+    def workspace(self, rows: int, dtype=torch.bfloat16, gradient: bool = True) -> torch.Tensor:
+        """A workspace for calls of up to `rows` rows of that type that follow
+        one another; without gradient for forward alone."""
+        return torch.empty(self.workspace_bytes(rows, dtype, gradient), dtype=torch.uint8,
+                           device=self._device)
+
+    def _call(self, name, hidden, weight, labels, loss, lse, grad_loss, d_hidden, d_weight,
+              grad_scale, accumulate, row_weights, workspace, stream):
+        if hidden.dtype not in _DTYPE:
+            _bad(name, "hidden must be float32, bfloat16 or float16")
+        dt, rows = hidden.dtype, hidden.shape[0]
+        full, head = torch.Size((rows, self.D)), torch.Size((self.V, self.D))
+        f32 = torch.float32
+        wt = dt if d_weight is None else d_weight.dtype
+        if wt is not dt and wt is not f32:
+            _bad(name, f"d_weight must be {dt} or float32")
+        ph, sh = self._matrix("hidden", hidden, dt, full, name)
+        pw, sw = self._matrix("weight", weight, dt, head, name)
+        pdh, sdh = self._matrix("d_hidden", d_hidden, dt, full, name)
+        pdw, sdw = self._matrix("d_weight", d_weight, wt, head, name)
+        args = _VOCAB_CE.pack(
+            ph, pw, self._vector("labels", labels, torch.int64, rows, name),
+            self._vector("row_weights", row_weights, f32, rows, name),
+            self._vector("loss", loss, f32, rows, name), self._vector("lse", lse, f32, rows, name),
+            self._vector("grad_loss", grad_loss, f32, rows, name), pdh, pdw,
+            sh, sw, sdh, sdw, rows, _DTYPE[dt], _DTYPE[wt], int(bool(accumulate)), grad_scale)
+        ws, ws_bytes = self._space(workspace, name)
+        _check(getattr(_lib, name)(self.handle, args, ws, ws_bytes,
+                                   _stream(stream, self._index)), name)
+
+    def forward(self, hidden, weight, labels, loss, lse=None, row_weights=None, workspace=None,
+                stream=None) -> None:
+        """loss [rows] float32, and lse [rows] float32 where a backward is to
+        follow.  hidden [rows, D], weight [V, D] (of one type), labels [rows]
+        int64 (negative: none), row_weights [rows] float32 or None."""
+        self._call("sgb_vocab_ce_forward", hidden, weight, labels, loss, lse, None, None, None,
+                   0.0, False, row_weights, workspace, stream)
+
+    def backward(self, hidden, weight, labels, lse, grad_loss=None, d_hidden=None, d_weight=None,
+                 grad_scale: float = 1.0, accumulate: bool = False, row_weights=None,
+                 workspace=None, stream=None) -> None:
+        """d_hidden [rows, D] in hidden's type and d_weight [V, D] in weight's
+        type or float32 (None: not wanted) of grad_scale * sum(grad_loss *
+        loss), from forward's lse; accumulate: d_weight is added to."""
+        self._call("sgb_vocab_ce_backward", hidden, weight, labels, None, lse, grad_loss, d_hidden,
+                   d_weight, grad_scale, accumulate, row_weights, workspace, stream)
+
+    def loss_grad(self, hidden, weight, labels, loss, d_hidden=None, d_weight=None,
+                  grad_scale: float = 1.0, accumulate: bool = False, lse=None, row_weights=None,
+                  workspace=None, stream=None) -> None:
+        """forward and backward (without grad_loss) in one go: one product less."""
+        self._call("sgb_vocab_ce_loss_grad", hidden, weight, labels, loss, lse, None, d_hidden,
+                   d_weight, grad_scale, accumulate, row_weights, workspace, stream)
+
+
+class Dropout(_Handle):
+    """Dropout with probability p (to 2^-16) from a counter-based generator:
+    the mask is a function of (seed, offset, row, column) and never stored."""
+    _kind = "dropout"
+
+    def __init__(self, p: float):
+        self.p = float(p)
+        self._create(self.p)
+
+    def _call(self, x, out, seed, offset, residual, state, first_row, stream):
+        w = "sgb_dropout_apply"
+        if x.dtype not in _DTYPE or out is None or out.dtype not in _DTYPE:
+            _bad(w, "x and out must be float32, bfloat16 or float16")
+        if x.dim() != 2:
+            _bad(w, "x must be a matrix")
+        shape, ot = x.shape, out.dtype
+        px, sx = self._matrix("x", x, x.dtype, shape, w)
+        pr, sr = self._matrix("residual", residual, ot, shape, w)
+        po, so = self._matrix("out", out, ot, shape, w)
+        args = _DROPOUT.pack(px, pr, po, self._vector("state", state, torch.int64, 2, w), sx, sr, so,
+                             shape[0], _int("first_row", first_row, 0, 2**62, w),
+                             _int("seed", seed, 0, 2**64, w), _int("offset", offset, 0, 2**64, w),
+                             _int("columns", shape[1], 0, 2**31, w), _DTYPE[x.dtype], _DTYPE[ot], 0)
+        _check(_lib.sgb_dropout_apply(self.handle, args, _stream(stream, self._index)), w)
+
+    def forward(self, x, out, seed: int = 0, offset: int = 0, residual=None, state=None,
+                first_row: int = 0, stream=None) -> None:
+        """out = residual + dropped x; x, out [rows, columns], residual in
+        out's type (x's, or float32) or None (0; out then in x's type).  out
+        may be x or residual.  state: two int64 on the device, the seed and
+        what is added to the offset, read when the kernel runs."""
+        self._call(x, out, seed, offset, residual, state, first_row, stream)
+
+    def backward(self, d_out, dx, seed: int = 0, offset: int = 0, state=None, first_row: int = 0,
+                 stream=None) -> None:
+        """dx (may be d_out) from d_out, in one type, under the forward's mask;
+        the residual's gradient is d_out."""
+        self._call(d_out, dx, seed, offset, None, state, first_row, stream)
+
+
+class QuantNorm(_Handle):
+    """x_out = x + h and the codes of rms(x_out) * weight in 8 bits ("int8", or
+    "fp8": e4m3) with a scale a row (group 0) or a group of columns."""
+    _kind = "quant_norm"
+
+    def __init__(self, D: int, weight=None, form: str = "int8", group: int = 0, eps: float = 1e-6):
+        w = "QuantNorm"
+        if form not in CODE:
+            _bad(w, f"unknown form {form!r}")
+        self.D, self.group = _int("D", D, -2**31, 2**31, w), _int("group", group, -2**31, 2**31, w)
+        self.form, self.weight = form, weight
+        self._code, self._type = CODE[form]
+        self._create(self.D, self._code, self.group, eps)
+        self.groups = -(-self.D // self.group) if self.group else 1
+
+    def forward(self, h, q, scales, x=None, x_out=None, stats=None, stream=None) -> None:
+        """h [rows, D]; x, x_out [rows, D] (float32, or h's type) or None; q
+        [rows, D] int8 or float8_e4m3fn; scales [rows, groups] float32; stats
+        [rows, 4] float32 or None (what a BlockNorm with post="none",
+        pre="rms" reads in its backward).  x_out may be x, or h."""
+        w = "sgb_quant_norm_forward"
+        if h.dtype not in _DTYPE:
+            _bad(w, "h must be float32, bfloat16 or float16")
+        if self.weight is None or self.weight.dtype not in _DTYPE:
+            _bad(w, "weight must be float32, bfloat16 or float16")
+        dt, rows, f32 = h.dtype, h.shape[0], torch.float32
+        rt = x.dtype if x is not None else x_out.dtype if x_out is not None else dt
+        if rt not in _DTYPE:
+            _bad(w, "x and x_out must be float32 or h's type")
+        shape = torch.Size((rows, self.D))
+        ph, sh = self._matrix("h", h, dt, shape, w)
+        px, sx = self._matrix("x", x, rt, shape, w)
+        po, so = self._matrix("x_out", x_out, rt, shape, w)
+        pq, sq = self._matrix("q", q, self._type, shape, w)
+        ps, ss = self._matrix("scales", scales, f32, torch.Size((rows, self.groups)), w)
+        args = _QUANT_NORM.pack(
+            ph, px, po, self._vector("weight", self.weight, self.weight.dtype, self.D, w), pq, ps,
+            self._vector("stats", stats, f32, 4 * rows, w), sh, sx, so, sq, ss, rows, _DTYPE[dt],
+            _DTYPE[rt], _DTYPE[self.weight.dtype], 0)
+        _check(_lib.sgb_quant_norm_forward(self.handle, args, _stream(stream, self._index)), w)
