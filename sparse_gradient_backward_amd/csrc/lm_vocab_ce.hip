@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <type_traits>
 
 #include "lm_internal.h"
 #include "sgb_lm_step.h"
@@ -51,46 +52,62 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 
 // ---------------------------------------------------------------- the product
 
-constexpr int kStep = 64;             // of the summed dimension a turn: 128 bytes a row
+constexpr int kStep = 64;  // of the summed dimension: 128 bytes a row
 constexpr int kRowBytes = kStep * 2;
 
-// A workgroup's tile of C (rows of A by rows of B), and a wave's.
-struct Big {
-  static constexpr int TM = 256, TN = 256, WM = 128, WN = 64;
+// A workgroup's tile of C (rows of A by rows of B), a wave's, and the steps that
+// are loaded between two barriers.
+struct Big {  // one workgroup a compute unit, for products that give each one
+  static constexpr int TM = 256, TN = 256, WM = 128, WN = 64, kSteps = 1;
 };
-struct Small {
-  static constexpr int TM = 128, TN = 64, WM = 64, WN = 32;
+struct Medium {  // two, one at its start or end while the other multiplies
+  static constexpr int TM = 128, TN = 128, WM = 64, WN = 64, kSteps = 1;
+};
+struct Tiny {  // for the time that loads take, not for how many there are
+  static constexpr int TM = 64, TN = 64, WM = 32, WN = 32, kSteps = 4;
 };
 template <typename C>
 constexpr int kThreadsOf = C::TM / C::WM * (C::TN / C::WN) * 64;
 
-enum Epilogue { kSums, kExps, kProbs, kAdd, kOut };
+enum Epilogue { kSums, kExps, kProbs, kGrads };
+
+// What says how much a row counts.
+struct Rows {
+  const int64_t* labels;
+  const float *weights, *above;  // null: ones
+  int64_t V;
+};
+__device__ __forceinline__ float factor_of(const Rows& q, int64_t r) {
+  const int64_t label = q.labels[r];
+  const float w = value_or(q.weights, r, 1.f), g = value_or(q.above, r, 1.f);
+  return w == 0.f || label < 0 || label >= q.V ? 0.f : w * g;
+}
 
 struct Product {
   const char *a, *b;
   int64_t lda, ldb;          // bytes from row to row; of 16
   int64_t plane_a, plane_b;  // bytes from one bf16 part of fp32 operands to the next
   int64_t M, N;              // rows of a, b
-  int steps, split;          // of the summed dimension, over `split` workgroups
+  int steps, split;          // of the summed dimension, over 1..steps workgroups
   int tm, tn;
+  Rows rows;
   // logits
   float2* stats;             // [vocabulary / WM][tokens]
   int64_t tokens;
-  const int64_t* labels;
   const float* lse;
   float* said;               // the label's logit
   void* exps;                // [tokens][ld_exps]
   int64_t ld_exps, v0, V;    // v0: the piece's first token of the vocabulary
-  // sums
-  float* sums;               // kAdd: [split][N][M]
+  // gradients: sums for a later kernel, or out
+  float* sums;               // [split][N][M] or null
   bool add;                  // to what is there
-  // out
-  void* out;                 // kOut: [N][ldo]
+  void* out;                 // [N][ldo]
   int64_t ldo;
   int out_dtype;
   const float* add_from;     // [N][M] or null
-  const float* most;         // times scale: what the sums are multiplied by
+  const float* most;         // (null: 1) times scale: what the sums are multiplied by
   float scale;
+  bool by_row;               // d_hidden: times the row's factor too, add_from with them
 };
 
 // Which bf16 parts (0: the highest) the products of fp32 operands are of, the
@@ -127,8 +144,11 @@ struct Stage {
   }
 };
 
+// Everything that this wave loads has arrived, and the others' too after the
+// barrier.  (The builtin, since the compiler counts loads to LDS itself, and
+// does not see a wait in assembly.)
 __device__ __forceinline__ void all_loaded() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
   __syncthreads();
 }
 
@@ -156,18 +176,52 @@ __device__ __forceinline__ F4 load4(const void* row, int64_t at, int64_t n) {
   return v;
 }
 
+// A wave's results on their way out, through LDS of its own: 32 of B's rows by
+// FRAGS times 32 of A's, put in as the matrix instruction leaves them (four
+// neighbours of a row a lane) and got as 16 bytes of whole rows, so that a store
+// fills lines.  Exponentials of 8192 x 131072 logits of 4096, bf16: 7.5 ms with
+// stores of what a lane holds, 7.3 so; of 1021 x 50021 of 1001, fp16: 175 and 163 us.
+template <typename O, int FRAGS>
+struct Rows32 {
+  static constexpr int kFrags = FRAGS, kRow = FRAGS * 32 * (int)sizeof(O), kPitch = kRow + 16;
+  static constexpr int kBytes = 32 * kPitch, kLanes = kRow / 16, kTurns = kLanes / 2;
+  typedef O Words __attribute__((ext_vector_type(16 / sizeof(O))));
+  static __device__ __forceinline__ void put(char* lds, int lane, int i, int k, F4 v) {
+    typedef O O4 __attribute__((ext_vector_type(4)));
+    const O4 o = {(O)v[0], (O)v[1], (O)v[2], (O)v[3]};
+    *reinterpret_cast<O4*>(lds + (lane & 31) * kPitch +
+                           (32 * i + 2 * k + 4 * (lane >> 5)) * (int)sizeof(O)) = o;
+  }
+  static __device__ __forceinline__ int row(int lane, int turn) {
+    return turn * (64 / kLanes) + lane / kLanes;
+  }
+  static __device__ __forceinline__ int col(int lane) {
+    return lane % kLanes * (16 / (int)sizeof(O));
+  }
+  static __device__ __forceinline__ Words get(const char* lds, int lane, int turn) {
+    return *reinterpret_cast<const Words*>(lds + row(lane, turn) * kPitch + lane % kLanes * 16);
+  }
+};
+
+// f of both halves of a wave.
+template <typename F>
+__device__ __forceinline__ float halves(float x, F f) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return f(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+
 template <typename E, int TERMS, int EPI, typename C>
-__global__ __launch_bounds__(kThreadsOf<C>, 2) void k_product(Product p) {
+__device__ __forceinline__ void product_tile(const Product& p, int block) {
   constexpr int TM = C::TM, TN = C::TN, WM = C::WM, WN = C::WN;
   constexpr int WAVES = kThreadsOf<C> / 64, FM = WM / 32, FN = WN / 32;
   constexpr int kBytes = (TM + TN) * kRowBytes;
-  __shared__ __attribute__((aligned(1024))) char buf0[kBytes];
-  __shared__ __attribute__((aligned(1024))) char buf1[kBytes];
+  // (variables of their own: a read of one does not wait for loads to the other)
+  __shared__ __attribute__((aligned(1024))) char buf0[C::kSteps * kBytes], buf1[C::kSteps * kBytes];
 
   // Workgroups go round the eight dies; each die gets a run of tiles of its
   // own, eight tiles of A by some of B at a time, whose operands its L2 shares.
   const int total = p.tm * p.tn * p.split, per = (total + 7) >> 3;
-  const int idx = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  const int idx = (block & 7) * per + (block >> 3);
   if (idx >= total) return;
   const int tiles = p.tm * p.tn;
   const int part = idx / tiles, in_part = idx % tiles;
@@ -184,25 +238,29 @@ __global__ __launch_bounds__(kThreadsOf<C>, 2) void k_product(Product p) {
   Stage<TN, WAVES> sb;
   sa.init(wave, lane, p.M - m0, p.lda);
   sb.init(wave, lane, p.N - n0, p.ldb);
-  const char* a = p.a + m0 * p.lda;
-  const char* b = p.b + n0 * p.ldb;
+  const char *a = p.a + m0 * p.lda, *b = p.b + n0 * p.ldb;
   const int from = (int)((int64_t)p.steps * part / p.split);
   const int to = (int)((int64_t)p.steps * (part + 1) / p.split);
-  const int turns = (to - from) * TERMS;
+  const int steps = (to - from) * TERMS, turns = (steps + C::kSteps - 1) / C::kSteps;
   int term = 0, step = from;
+  // The next steps' loads; past the last, that one's once more.  (A load that is
+  // made only now and then makes the compiler wait for all of them.)
   const auto stage = [&](char* buf) {
-    const int64_t at = (int64_t)step * kRowBytes;
-    const char *pa = a + at, *pb = b + at;
-    if (TERMS > 1) {
-      pa += (kPartsA >> (2 * term) & 3) * p.plane_a;
-      pb += (kPartsB >> (2 * term) & 3) * p.plane_b;
+#pragma unroll
+    for (int s = 0; s < C::kSteps; ++s) {
+      const int64_t at = (int64_t)step * kRowBytes;
+      const char *pa = a + at, *pb = b + at;
+      if (TERMS > 1) {
+        pa += (kPartsA >> (2 * term) & 3) * p.plane_a;
+        pb += (kPartsB >> (2 * term) & 3) * p.plane_b;
+      }
+      sa.load(pa, buf + s * kBytes, wave);
+      sb.load(pb, buf + s * kBytes + TM * kRowBytes, wave);
+      const bool wrap = step + 1 == to, on = !wrap || term + 1 < TERMS;
+      term += wrap && on;
+      step = wrap ? (on ? from : step) : step + 1;
     }
-    sa.load(pa, buf, wave);
-    sb.load(pb, buf + TM * kRowBytes, wave);
-    if (++step == to) {
-      step = from;
-      ++term;
-    }
+    __builtin_amdgcn_sched_barrier(0);  // (the compiler would put them off)
   };
 
   Acc acc[FM][FN];
@@ -213,155 +271,214 @@ __global__ __launch_bounds__(kThreadsOf<C>, 2) void k_product(Product p) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
 
+  // A step is four of 16, each with its fragments read while the step before
+  // multiplies.  A turn's last products come after the barrier that frees its
+  // buffer, and cover the next turn's first reads.
+  typedef typename Vec<E>::type V8;
+  V8 fa[2][FM], fb[2][FN];
   const int key = (lane >> 1) & 7, row = (lane & 31) * kRowBytes;
-  const auto compute = [&](const char* buf) {
-    typedef typename Vec<E>::type V8;
-    const char* la = buf + wm * kRowBytes + row;
-    const char* lb = buf + (TM + wn) * kRowBytes + row;
+  const auto read = [&](const char* buf, int kk) {
+    const int at = row + ((kk * 2 + (lane >> 5)) ^ key) * 16;
+    const uint32_t ra = wm * kRowBytes + at, rb = (TM + wn) * kRowBytes + at;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const int at = ((kk * 2 + (lane >> 5)) ^ key) * 16;
-      V8 fa[FM], fb[FN];
+    for (int i = 0; i < FM; ++i)
+      fa[kk & 1][i] = *reinterpret_cast<const V8*>(buf + (ra + i * 32 * kRowBytes));
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-        fa[i] = *reinterpret_cast<const V8*>(la + at + i * 32 * kRowBytes);
+    for (int j = 0; j < FN; ++j)
+      fb[kk & 1][j] = *reinterpret_cast<const V8*>(buf + (rb + j * 32 * kRowBytes));
+  };
+  const auto multiply = [&](int kk) {
+    constexpr int kEach = FM * FN / (FM + FN);
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        fb[j] = *reinterpret_cast<const V8*>(lb + at + j * 32 * kRowBytes);
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+      for (int j = 0; j < FN; ++j) acc[i][j] = mfma(fa[kk & 1][i], fb[kk & 1][j], acc[i][j]);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma(fa[i], fb[j], acc[i][j]);
+    for (int i = 0; i < FM + FN; ++i) {  // one read, then one or more products
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, FM * FN - kEach * (FM + FN), 0);
+  };
+  // a turn's steps but the last of their products
+  const auto three = [&](const char* buf) {
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      read(buf, kk + 1);
+      multiply(kk);
+    }
+  };
+  const auto turn = [&](const char* buf) {
+#pragma unroll
+    for (int s = 0; s < C::kSteps; ++s) {
+      three(buf + s * kBytes);
+      if (s + 1 == C::kSteps) break;
+      read(buf + (s + 1) * kBytes, 0);
+      multiply(3);
     }
   };
 
-  if (turns > 0) stage(buf0);
+  stage(buf0);
+  stage(buf1);
+  all_loaded();
+  read(buf0, 0);
   int left = turns;
-  for (; left >= 2; left -= 2) {
+  for (; left > 2; left -= 2) {
+    turn(buf0);
+    all_loaded();
+    stage(buf0);
+    read(buf1, 0);
+    multiply(3);
+    turn(buf1);
     all_loaded();
     stage(buf1);
-    compute(buf0);
-    all_loaded();
-    if (left > 2) stage(buf0);
-    compute(buf1);
+    read(buf0, 0);
+    multiply(3);
   }
-  if (left) {
+  if (left > 1) {
+    turn(buf0);
     all_loaded();
-    compute(buf0);
+    read(buf1, 0);
+    multiply(3);
   }
+  const char* buf = left > 1 ? buf1 : buf0;
+  three(buf);
+  for (int s = (turns - 1) * C::kSteps + 1; s < steps; ++s) {  // (none where a turn is one step)
+    buf += kBytes;
+    read(buf, 0);
+    multiply(3);
+    three(buf);
+  }
+  multiply(3);
+  all_loaded();  // LDS is free: no load to it is under way any more
 
   // acc[i][j][k]: C's row (of A) m0 + wm + 32 i + 8 (k / 4) + 4 (lane / 32) +
   // k % 4, its column (of B) n0 + wn + 32 j + lane % 32
   const int64_t mw = m0 + wm + 4 * (lane >> 5);
+  char* own = (wave < WAVES / 2 ? buf0 : buf1) + wave % (WAVES / 2) * Rows32<float, 2>::kBytes;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int64_t n = n0 + wn + 32 * j + (lane & 31);
+    __builtin_amdgcn_sched_barrier(0);  // (both at once would spill)
+    const int64_t nw = n0 + wn + 32 * j, n = nw + (lane & 31);
     const bool there = n < p.N;
-    if (EPI == kSums || EPI == kExps) {
-      typedef typename std::conditional<__is_same(E, bf16_t) && TERMS == 1, f16_t, float>::type X;
-      if (m0 + wm + WM > p.M) {  // past the vocabulary
+    if constexpr (EPI == kGrads) {
+      float by = 1.f;
+      if (!p.sums)
+        by = p.scale * (!p.by_row ? value_or(p.most, 0, 1.f) : there ? factor_of(p.rows, n) : 0.f);
+      typedef Rows32<float, (FM > 1 ? 2 : 1)> L;
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+      for (int i0 = 0; i0 < FM; i0 += L::kFrags) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (mw + 32 * i + 8 * (k >> 2) + (k & 3) >= p.M) acc[i][j][k] = -INFINITY;
-      }
-      const int64_t label = there ? p.labels[n] - (p.v0 + m0 + wm) : -1;
-      if (label >= 0 && label < WM && label + m0 + wm < p.M) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (label == 32 * i + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3))
-              p.said[n] = acc[i][j][k];
-      }
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) top = fmaxf(top, acc[i][j][k]);
-      const auto halves = [](float x, auto f) {
-        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x),
-                                                        false, false);
-        return f(__uint_as_float(s[0]), __uint_as_float(s[1]));
-      };
-      top = halves(top, [](float x, float y) { return fmaxf(x, y); });
-      if (top == -INFINITY) top = 0.f;  // nothing but -inf: the sum is 0
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float e = exp2_((acc[i][j][k] - top) * kLog2e);
-          acc[i][j][k] = e;
-          sum += e;
-        }
-      sum = halves(sum, [](float x, float y) { return x + y; });
-      if (there && lane < 32)
-        p.stats[(p.v0 + m0 + wm) / WM * p.tokens + n] = make_float2(top, sum);
-      if (EPI == kExps && there) {
-        X* out = static_cast<X*>(p.exps) + n * p.ld_exps;
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int i = 0; i < L::kFrags; ++i)
 #pragma unroll
           for (int k = 0; k < 16; k += 4) {
-            constexpr float up = sizeof(X) == 2 ? kUp : 1.f;
-            const F4 v = {acc[i][j][k] * up, acc[i][j][k + 1] * up, acc[i][j][k + 2] * up,
-                          acc[i][j][k + 3] * up};
-            store4<X>(out, p.v0 + mw + 32 * i + 2 * k, v, 4);
+            const Acc& c = acc[i0 + i][j];
+            L::put(own, lane, i, k, F4{c[k], c[k + 1], c[k + 2], c[k + 3]});
           }
-      }
-    } else if (EPI == kProbs) {
-      typedef typename std::conditional<__is_same(E, bf16_t) && TERMS == 1, f16_t, float>::type X;
-      if (!there) continue;
-      const float lse = p.lse[n];
-      constexpr float up = sizeof(X) == 2 ? kUp : 1.f;
-      X* out = static_cast<X*>(p.exps) + n * p.ld_exps;
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          F4 v;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) v[u] = exp2_((acc[i][j][k + u] - lse) * kLog2e) * up;
-          store4<X>(out, p.v0 + mw + 32 * i + 2 * k, v, 4);
-        }
-    } else if (EPI == kAdd) {
-      if (!there) continue;
-      float* out = p.sums + ((int64_t)part * p.N + n) * p.M;
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          const int64_t m = mw + 32 * i + 2 * k;
-          if (m >= p.M) continue;
-          F4 v = {acc[i][j][k], acc[i][j][k + 1], acc[i][j][k + 2], acc[i][j][k + 3]};
-          if (p.add) v += load4<float>(out, m, p.M - m);
-          store4<float>(out, m, v, p.M - m);
-        }
-    } else {
-      if (!there) continue;
-      const float by = p.scale * *p.most;
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          const int64_t m = mw + 32 * i + 2 * k, n4 = p.M - m;
-          if (n4 <= 0) continue;
-          F4 v = {acc[i][j][k], acc[i][j][k + 1], acc[i][j][k + 2], acc[i][j][k + 3]};
-          v *= by;
-          if (p.add_from) v += load4<float>(p.add_from + n * p.M, m, n4);
+        for (int u = 0; u < L::kTurns; ++u) {
+          const int r = L::row(lane, u);
+          const float scale = __shfl(by, r);
+          const int64_t at = nw + r, m = m0 + wm + 32 * i0 + L::col(lane), n4 = p.M - m;
+          F4 v = L::get(own, lane, u);
+          if (at >= p.N || n4 <= 0) continue;
+          if (p.sums) {
+            float* out = p.sums + ((int64_t)part * p.N + at) * p.M;
+            if (p.add) v += load4<float>(out, m, n4);
+            store4<float>(out, m, v, n4);
+            continue;
+          }
+          F4 more = {0.f, 0.f, 0.f, 0.f};
+          if (p.add_from) more = load4<float>(p.add_from + at * p.M, m, n4);
+          if (p.by_row)
+            v = scale == 0.f ? F4{0.f, 0.f, 0.f, 0.f} : (v + more) * scale;
+          else
+            v = v * scale + more;
           if (p.out_dtype == SGB_F32) {
-            float* out = static_cast<float*>(p.out) + n * p.ldo;
+            float* out = static_cast<float*>(p.out) + at * p.ldo;
             if (p.add) v += load4<float>(out, m, n4);
             store4<float>(out, m, v, n4);
           } else {
-            E* out = static_cast<E*>(p.out) + n * p.ldo;
+            E* out = static_cast<E*>(p.out) + at * p.ldo;
             if (p.add) v += load4<E>(out, m, n4);
             store4<E>(out, m, v, n4);
           }
         }
+      }
+    } else {
+      typedef typename std::conditional<__is_same(E, bf16_t) && TERMS == 1, f16_t, float>::type X;
+      float top = 0.f, sum = 0.f;
+      if constexpr (EPI == kProbs) {
+        if (there) top = p.lse[n];
+      } else {
+        if (m0 + wm + WM > p.M) {  // past the vocabulary
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (mw + 32 * i + 8 * (k >> 2) + (k & 3) >= p.M) acc[i][j][k] = -INFINITY;
+        }
+        const int64_t label = there ? p.rows.labels[n] - (p.v0 + m0 + wm) : -1;
+        if (label >= 0 && label < WM && label + m0 + wm < p.M) {
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (label == 32 * i + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3))
+                p.said[n] = acc[i][j][k];
+        }
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) top = fmaxf(top, acc[i][j][k]);
+        top = halves(top, [](float x, float y) { return fmaxf(x, y); });
+        if (top == -INFINITY) top = 0.f;  // nothing but -inf: the sum is 0
+      }
+      typedef Rows32<X, (FM < 8 / (int)sizeof(X) ? FM : 8 / (int)sizeof(X))> L;
+#pragma unroll
+      for (int i0 = 0; i0 < FM; i0 += L::kFrags) {
+#pragma unroll
+        for (int i = 0; i < L::kFrags; ++i)
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            F4 v;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              v[u] = exp2_((acc[i0 + i][j][k + u] - top) * kLog2e);
+              sum += v[u];
+            }
+            if (EPI != kSums) L::put(own, lane, i, k, v * (sizeof(X) == 2 ? kUp : 1.f));
+          }
+        if constexpr (EPI != kSums) {
+#pragma unroll
+          for (int u = 0; u < L::kTurns; ++u) {
+            const int64_t at = nw + L::row(lane, u);
+            const auto v = L::get(own, lane, u);
+            if (at >= p.N) continue;
+            X* out = static_cast<X*>(p.exps) + at * p.ld_exps + (p.v0 + m0 + wm + 32 * i0 + L::col(lane));
+            *reinterpret_cast<typename L::Words*>(out) = v;
+          }
+        }
+      }
+      if constexpr (EPI != kProbs) {
+        sum = halves(sum, [](float x, float y) { return x + y; });
+        if (there && lane < 32)
+          p.stats[(p.v0 + m0 + wm) / WM * p.tokens + n] = make_float2(top, sum);
+      }
     }
   }
+}
+
+// `q`: a second product of the same kind, in workgroups from `first` on.
+template <typename E, int TERMS, int EPI, typename C>
+__global__ __launch_bounds__(kThreadsOf<C>, 2) void k_product(Product p, Product q, int first) {
+  int block = (int)blockIdx.x;
+  if (block >= first) {
+    p = q;
+    block -= first;
+  }
+  product_tile<E, TERMS, EPI, C>(p, block);
 }
 
 // ---------------------------------------------------------------- copies
@@ -389,222 +506,253 @@ struct Parts<float> {
   }
 };
 
-// [rows][D] to [rows][pitch], zeros past D.
-template <typename T>
-__global__ __launch_bounds__(256) void k_rows(const T* src, int64_t stride, int64_t rows, int D,
-                                              typename Parts<T>::E* dst, int64_t pitch,
-                                              int64_t plane) {
-  typedef typename Parts<T>::E E;
-  constexpr int P = Parts<T>::kCount;
-  const int64_t groups = pitch / 8, all = rows * groups;
-  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < all; g += (int64_t)gridDim.x * 256) {
-    const int64_t r = g / groups;
-    const int c = (int)(g % groups) * 8;
-    E out[P][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      E e[P];
-      Parts<T>::split(c + i < D ? src[r * stride + c + i] : (T)0.f, e);
-#pragma unroll
-      for (int k = 0; k < P; ++k) out[k][i] = e[k];
-    }
-#pragma unroll
-    for (int k = 0; k < P; ++k)
-      *reinterpret_cast<uint4*>(dst + k * plane + r * pitch + c) =
-          *reinterpret_cast<const uint4*>(out[k]);
-  }
-}
-
 constexpr int kTile = 64;
 
-// [rows][D] to [D][pitch], zeros from `rows` to `pitch` and for rows whose
-// factor is 0 (what they hold may be no number).
-template <typename T>
-__global__ __launch_bounds__(256) void k_transpose(const T* src, int64_t stride, int64_t rows,
-                                                   int D, const float* factors,
-                                                   typename Parts<T>::E* dst, int64_t pitch,
-                                                   int64_t plane) {
+template <typename T, typename V>
+__device__ __forceinline__ void store_parts(const V (&v)[8], typename Parts<T>::E* to, int64_t plane) {
   typedef typename Parts<T>::E E;
   constexpr int P = Parts<T>::kCount;
-  __shared__ T tile[kTile][kTile + 4 / sizeof(T)];
-  const int across = (D + kTile - 1) / kTile;
-  const int64_t r0 = (int64_t)(blockIdx.x / across) * kTile;
-  const int d0 = (int)(blockIdx.x % across) * kTile;
+  E out[P][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    E e[P];
+    Parts<T>::split((T)v[i], e);
+#pragma unroll
+    for (int k = 0; k < P; ++k) out[k][i] = e[k];
+  }
+#pragma unroll
+  for (int k = 0; k < P; ++k)
+    *reinterpret_cast<uint4*>(to + k * plane) = *reinterpret_cast<const uint4*>(out[k]);
+}
+
+// An operand's rows [rows][D] as the product reads them: [rows][pitch] with zeros
+// past D, transposed to [D][pitch_t] with zeros past the last row (and, with
+// `only`, in rows that do not count: what they hold may be no number), or both.
+template <typename T>
+struct Copy {
+  typedef typename Parts<T>::E E;
+  const T* src;
+  int64_t stride, rows;
+  int D;
+  E *to, *to_t;  // or null
+  int64_t pitch, plane, pitch_t, plane_t;
+  bool only;
+  Rows count;
+};
+
+// Tiles of 64 x 64, of `a` in the first workgroups and of `b` in the others.
+template <typename T>
+__global__ __launch_bounds__(256) void k_copy(Copy<T> a, Copy<T> b, unsigned first) {
+  __shared__ __attribute__((aligned(16))) T tile[kTile][kTile + 4 / sizeof(T)];
+  unsigned block = blockIdx.x;
+  if (block >= first) {
+    a = b;
+    block -= first;
+  }
+  const unsigned across = (unsigned)((a.D + kTile - 1) / kTile);
+  const int64_t r0 = (int64_t)(block / across) * kTile;
+  const int d0 = (int)(block % across) * kTile;
   const int t = (int)threadIdx.x;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = (t >> 3) + 32 * u, c = (t & 7) * 8;
-    const T* from = src + (r0 + r) * stride + d0 + c;
-    const bool on = r0 + r < rows && (!factors || factors[r0 + r] != 0.f);
-    const int n = on ? min(8, D - d0 - c) : 0;
-    const Raw8<T> raw = load8(from, n);
-    T v[8];
-    __builtin_memcpy(v, &raw, sizeof v);
+    const bool there = r0 + r < a.rows;
+    Raw8<T> raw = load8(a.src + (r0 + r) * a.stride + d0 + c, there ? min(8, a.D - d0 - c) : 0);
+    if (a.to && there) {
+      T v[8];
+      __builtin_memcpy(v, &raw, sizeof v);
+      store_parts<T>(v, a.to + (r0 + r) * a.pitch + d0 + c, a.plane);
+    }
+    const bool on = there && (!a.only || factor_of(a.count, r0 + r) != 0.f);
+    uint32_t* row = reinterpret_cast<uint32_t*>(&tile[r][c]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tile[r][c + i] = v[i];
+    for (int i = 0; i < Vec<T>::kWords; ++i) row[i] = on ? raw.w[i] : 0u;
   }
+  if (!a.to_t) return;
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int d = (t >> 3) + 32 * u, c = (t & 7) * 8;
-    if (d0 + d >= D) continue;
-    E out[P][8];
+    if (d0 + d >= a.D) continue;
+    T v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      E e[P];
-      Parts<T>::split(tile[c + i][d], e);
-#pragma unroll
-      for (int k = 0; k < P; ++k) out[k][i] = e[k];
-    }
-#pragma unroll
-    for (int k = 0; k < P; ++k)
-      *reinterpret_cast<uint4*>(dst + k * plane + (int64_t)(d0 + d) * pitch + r0 + c) =
-          *reinterpret_cast<const uint4*>(out[k]);
+    for (int i = 0; i < 8; ++i) v[i] = tile[c + i][d];
+    store_parts<T>(v, a.to_t + (int64_t)(d0 + d) * a.pitch_t + r0 + c, a.plane_t);
   }
 }
 
 // ---------------------------------------------------------------- row work
 
-// A row's factor (0 where it does not count), and the largest magnitude of them
-// all: d_weight's operand carries factor / largest, which no type's range can
-// lose, d_hidden the factor itself at its end.
-__global__ __launch_bounds__(1024) void k_factors(const int64_t* labels, const float* weights,
-                                                  const float* above, int64_t rows, int64_t V,
-                                                  float* factors, float* most, Header* hdr,
-                                                  uint32_t epoch) {
+// The largest magnitude of the rows' factors.  fp16 gradients for d_weight carry
+// the factor over it, so that none leaves the type's range.
+__global__ __launch_bounds__(1024) void k_most(Rows q, int64_t rows, float* most) {
   __shared__ float part[16];
   float top = 0.f;
-  bool bad = false;
-  for (int64_t r = threadIdx.x; r < rows; r += 1024) {
-    const int64_t label = labels[r];
-    const float w = value_or(weights, r, 1.f), g = value_or(above, r, 1.f);
-    bad |= w != 0.f && label >= V;
-    const float f = w == 0.f || label < 0 || label >= V ? 0.f : w * g;
-    factors[r] = f;
-    top = fmaxf(top, fabsf(f));
-  }
-  if (bad) set_status(hdr, epoch, SGB_ERR_INDEX_OUT_OF_RANGE);
+  for (int64_t r = threadIdx.x; r < rows; r += 1024) top = fmaxf(top, fabsf(factor_of(q, r)));
   top = wave_max(top);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
   __syncthreads();
   if (threadIdx.x < 64) {
     top = wave_max(threadIdx.x < 16 ? part[threadIdx.x] : 0.f);
-    if (threadIdx.x == 0) {
-      *most = top;
-      hdr->epoch = epoch;
-    }
+    if (threadIdx.x == 0) *most = top;
   }
 }
 
-// The waves' sums of a row to its log-sum-exp and loss: 16 rows a workgroup.
-__global__ __launch_bounds__(256) void k_lse(const float2* stats, int parts, int64_t tokens,
-                                             const int64_t* labels, const float* weights,
-                                             const float* said, int64_t V, float* loss, float* lse,
-                                             Header* hdr, uint32_t epoch) {
-  __shared__ float2 all[16][17];
-  const int who = (int)threadIdx.x & 15, share = (int)threadIdx.x >> 4;
-  const int64_t r = (int64_t)blockIdx.x * 16 + who;
+// A reference and a sum of exponentials relative to it.
+struct Sum {
   float m = -INFINITY, s = 0.f;
-  const auto add = [&](float2 v) {
+  __device__ __forceinline__ void add(float2 v) {
     if (v.y == 0.f) return;  // no mass, whatever its reference
     const float top = fmaxf(m, v.x);
     s = s * exp2_((m - top) * kLog2e) + v.y * exp2_((v.x - top) * kLog2e);
     m = top;
-  };
-  if (r < tokens) {
-    int i = share;
-    for (; i + 112 < parts; i += 128) {
+  }
+  // every `by`th of the waves' sums of a row, from `i` on
+  __device__ __forceinline__ void add_all(const float2* stats, int parts, int64_t tokens, int64_t r,
+                                          int i, int by) {
+    for (; i + 7 * by < parts; i += 8 * by) {
       float2 v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = stats[(int64_t)(i + 16 * u) * tokens + r];
+      for (int u = 0; u < 8; ++u) v[u] = stats[(int64_t)(i + by * u) * tokens + r];
 #pragma unroll
       for (int u = 0; u < 8; ++u) add(v[u]);
     }
-    for (; i < parts; i += 16) add(stats[(int64_t)i * tokens + r]);
+    for (; i < parts; i += by) add(stats[(int64_t)i * tokens + r]);
   }
-  all[share][who] = make_float2(m, s);
+  __device__ __forceinline__ float log() const { return m + logf(s); }
+};
+
+// Where a row's log-sum-exp and loss go.
+struct Loss {
+  const float2* stats;
+  int parts;
+  int64_t tokens;
+  Rows rows;
+  const float* said;
+  float *loss, *lse;
+  Header* hdr;
+  uint32_t epoch;
+};
+
+__device__ __forceinline__ void mark(const Rows& q, int64_t r, Header* hdr, uint32_t epoch) {
+  if (q.labels[r] >= q.V && value_or(q.weights, r, 1.f) != 0.f)
+    set_status(hdr, epoch, SGB_ERR_INDEX_OUT_OF_RANGE);
+}
+__device__ __forceinline__ void finish_row(const Loss& q, int64_t r, float lse) {
+  q.lse[r] = lse;
+  const float f = factor_of(q.rows, r);
+  q.loss[r] = f == 0.f ? 0.f : f * (lse - q.said[r]);
+  mark(q.rows, r, q.hdr, q.epoch);
+}
+
+constexpr int kFewParts = 64;  // sums of a row that k_grad adds up itself
+constexpr int kShares = 16;  // of a row's sums, each added up alone and then in turn
+
+// 16 rows a workgroup.
+__global__ __launch_bounds__(256) void k_lse(Loss q) {
+  __shared__ float2 all[kShares][17];
+  const int who = (int)threadIdx.x & 15, share = (int)threadIdx.x >> 4;
+  const int64_t r = (int64_t)blockIdx.x * 16 + who;
+  Sum mine;
+  if (r < q.tokens) mine.add_all(q.stats, q.parts, q.tokens, r, share, kShares);
+  all[share][who] = make_float2(mine.m, mine.s);
   __syncthreads();
-  if (threadIdx.x < 16 && r < tokens) {
-    m = -INFINITY;
-    s = 0.f;
-    for (int i = 0; i < 16; ++i) add(all[i][who]);
-    const float l = m + logf(s);
-    if (lse) lse[r] = l;
-    const float w = value_or(weights, r, 1.f);
-    const int64_t label = labels[r];
-    if (w != 0.f && label >= V) set_status(hdr, epoch, SGB_ERR_INDEX_OUT_OF_RANGE);
-    if (loss) loss[r] = w == 0.f || label < 0 || label >= V ? 0.f : w * (l - said[r]);
+  if (threadIdx.x < 16 && r < q.tokens) {
+    Sum sum;
+    for (int i = 0; i < kShares; ++i) sum.add(all[i][who]);
+    finish_row(q, r, sum.log());
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) hdr->epoch = epoch;
+  if (blockIdx.x == 0 && threadIdx.x == 0) q.hdr->epoch = q.epoch;
 }
 
 struct Grad {
-  const void* exps;      // [tokens][ld_exps], the chunk's
-  int64_t ld_exps, tokens;
-  const float2* stats;   // null: relative to the row's lse already
-  int wave_cols;
+  const void* exps;  // [tokens][ld_exps], the chunk's
+  int64_t ld_exps;
+  int wave_cols;     // of a wave's reference; 0: they are relative to the row's lse
+  Loss rows;         // the chunk's; SUM: their lse and loss are found here
   const float* lse;
-  const int64_t* labels;
-  const float *factors, *most;
-  int64_t v0, width, V;  // the piece
-  void* g;               // [tokens][pitch] or null
-  void* gt;              // [width][pitch_t] or null
+  const float* most;  // null: 1
+  int64_t v0, width;  // the piece
+  void *g, *gt;       // [tokens][pitch], [width][pitch_t], or null
   int64_t pitch, plane, pitch_t, plane_t;
 };
 
 // The gradient of a piece's logits from their exponentials: as it is (over the
 // row's factor) and transposed (with it), in the operands' type, zeros past the
 // vocabulary and past the last token.
-template <typename T, typename X>
+template <typename T, typename X, bool SUM>
 __global__ __launch_bounds__(256) void k_grad(Grad q) {
   typedef typename Parts<T>::E E;
-  constexpr int P = Parts<T>::kCount;
   constexpr float kBy = __is_same(T, f16_t) ? kUp : 1.f;  // fp16 has no room below 2^-24
   __shared__ float tile[kTile][kTile + 1];
-  const int across = (int)(q.pitch / kTile);
+  __shared__ float2 part[SUM ? kShares : 1][SUM ? kTile : 1];
+  const unsigned across = (unsigned)(q.pitch / kTile);
   const int64_t r0 = (int64_t)(blockIdx.x / across) * kTile;
   const int64_t c0 = (int64_t)(blockIdx.x % across) * kTile;
   const int t = (int)threadIdx.x;
-  const float most = *q.most;
+  const int64_t tokens = q.rows.tokens;
+  // what this thread needs of its two rows, asked for at once
+  const int c = (t & 7) * 8;
+  const int64_t at = q.v0 + c0 + c;
+  Raw8<X> raw[2];
+  float f[2], top[2], lse[2];
+  int64_t label[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int lr = (t >> 3) + 32 * u, c = (t & 7) * 8;
-    const int64_t r = r0 + lr;
-    float v[8];
+    const int64_t r = min(r0 + (t >> 3) + 32 * u, tokens - 1);
+    raw[u] = *reinterpret_cast<const Raw8<X>*>(static_cast<const X*>(q.exps) + r * q.ld_exps + at);
+    top[u] = q.wave_cols ? q.rows.stats[at / q.wave_cols * tokens + r].x : 0.f;
+    lse[u] = SUM ? 0.f : q.lse[r];
+    f[u] = factor_of(q.rows.rows, r);
+    label[u] = q.rows.rows.labels[r] - at;
+  }
+  const float most = value_or(q.most, 0, 1.f);
+  if constexpr (SUM) {
+    // (in k_lse's order: both give the same bits)
+    const int64_t r = r0 + (t & 63);
+    float2 v[kShares / 4][kFewParts / kShares];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    float share = 0.f;
-    if (r < q.tokens) {
-      const float f = q.factors[r];
-      if (f != 0.f) {
-        const int64_t at = q.v0 + c0 + c;
-        const int n = (int)min((int64_t)8, q.v0 + q.width - at);
-        share = f / most;
-        float k = sizeof(X) == 2 ? 1.f / kUp : 1.f;
-        if (q.stats)
-          k *= exp2_((q.stats[at / q.wave_cols * q.tokens + r].x - q.lse[r]) * kLog2e);
-        const int64_t label = q.labels[r] - at;
-        float e[8];
-        widen8(*reinterpret_cast<const Raw8<X>*>(static_cast<const X*>(q.exps) + r * q.ld_exps + at), e);
+    for (int u = 0; u < kShares / 4; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < n) v[i] = (e[i] * k - (label == i ? 1.f : 0.f)) * kBy;
+      for (int i = 0; i < kFewParts / kShares; ++i) {
+        const int at = (t >> 6) + 4 * u + kShares * i;
+        v[u][i] = r < tokens && at < q.rows.parts ? q.rows.stats[at * tokens + r] : float2{0.f, 0.f};
       }
-      if (q.g) {
-        E out[P][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          E e[P];
-          Parts<T>::split((T)v[i], e);
+    for (int u = 0; u < kShares / 4; ++u) {
+      Sum mine;
 #pragma unroll
-          for (int k = 0; k < P; ++k) out[k][i] = e[k];
-        }
-#pragma unroll
-        for (int k = 0; k < P; ++k)
-          *reinterpret_cast<uint4*>(static_cast<E*>(q.g) + k * q.plane + r * q.pitch + c0 + c) =
-              *reinterpret_cast<const uint4*>(out[k]);
-      }
+      for (int i = 0; i < kFewParts / kShares; ++i) mine.add(v[u][i]);
+      part[(t >> 6) + 4 * u][t & 63] = make_float2(mine.m, mine.s);
     }
+    __syncthreads();
+    if (t < 64) {
+      Sum sum;
+      for (int i = 0; i < kShares; ++i) sum.add(part[i][t]);
+      const float lse = sum.log();
+      part[0][t].x = lse;
+      if (c0 == 0 && r < tokens) finish_row(q.rows, r, lse);
+    }
+    __syncthreads();
+  } else if (q.wave_cols == 0 && q.v0 + c0 == 0 && t < 64 && r0 + t < tokens) {
+    mark(q.rows.rows, r0 + t, q.rows.hdr, q.rows.epoch);
+  }
+  if (blockIdx.x == 0 && t == 0) q.rows.hdr->epoch = q.rows.epoch;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int lr = (t >> 3) + 32 * u;
+    const bool there = r0 + lr < tokens;
+    const int n = (int)min((int64_t)8, q.v0 + q.width - at);
+    float k = sizeof(X) == 2 ? 1.f / kUp : 1.f;
+    if (q.wave_cols) k *= exp2_((top[u] - (SUM ? part[0][lr].x : lse[u])) * kLog2e);
+    const bool on = there && f[u] != 0.f;
+    const float share = on ? f[u] / most : 0.f;
+    float v[8], e[8];
+    widen8(raw[u], e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = on && i < n ? (e[i] * k - (label[u] == i ? 1.f : 0.f)) * kBy : 0.f;
+    if (q.g && there) store_parts<T>(v, static_cast<E*>(q.g) + (r0 + lr) * q.pitch + c0 + c, q.plane);
 #pragma unroll
     for (int i = 0; i < 8; ++i) tile[lr][c + i] = v[i] * share;
   }
@@ -614,33 +762,25 @@ __global__ __launch_bounds__(256) void k_grad(Grad q) {
   for (int u = 0; u < 2; ++u) {
     const int lv = (t >> 3) + 32 * u, c = (t & 7) * 8;
     if (c0 + lv >= q.width) continue;
-    E out[P][8];
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      E e[P];
-      Parts<T>::split((T)tile[c + i][lv], e);
-#pragma unroll
-      for (int k = 0; k < P; ++k) out[k][i] = e[k];
-    }
-#pragma unroll
-    for (int k = 0; k < P; ++k)
-      *reinterpret_cast<uint4*>(static_cast<E*>(q.gt) + k * q.plane_t + (c0 + lv) * q.pitch_t + r0 + c) =
-          *reinterpret_cast<const uint4*>(out[k]);
+    for (int i = 0; i < 8; ++i) v[i] = tile[c + i][lv];
+    store_parts<T>(v, static_cast<E*>(q.gt) + (c0 + lv) * q.pitch_t + r0 + c, q.plane_t);
   }
 }
 
 // d_hidden: the parts' sums in their order, the row's factor, one rounding.
 template <typename T>
 __global__ __launch_bounds__(256) void k_join(const float* sums, int split, int64_t rows, int D,
-                                              const float* factors, float scale, T* out,
-                                              int64_t stride) {
+                                              Rows count, float scale, T* out, int64_t stride) {
   const int64_t groups = (D + 7) / 8, all = rows * groups;
   for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < all; g += (int64_t)gridDim.x * 256) {
     const int64_t r = g / groups;
     const int c = (int)(g % groups) * 8, n = min(8, D - c);
-    const float f = factors[r];
+    const float f = factor_of(count, r);
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (f != 0.f) {
+#pragma unroll 4
       for (int s = 0; s < split; ++s) {
         float x[8];
         widen8(load8(sums + ((int64_t)s * rows + r) * D + c, n), x);
@@ -673,43 +813,74 @@ struct sgb_vocab_ce_s {
 
 namespace {
 
-constexpr int64_t kExpBytes = 1ll << 30;     // a chunk's exponentials
+constexpr int64_t kExpBytes = 1ll << 31;     // a chunk's exponentials
 constexpr int64_t kStatBytes = 1ll << 28;    // their sums
 constexpr int64_t kPieceElems = 1ll << 27;   // a piece's copies
-constexpr int kMaxSplit = 16;
+constexpr int kMaxSplit = 32;
 
 int64_t up(int64_t n, int64_t to) { return div_up(n, to) * to; }
-
-// What a call lays out in its workspace.
-struct Layout {
-  int parts;           // of an element
-  bool copy;           // fp32 operands are always copied (others where their rows ask for it)
-  int64_t chunk, pad;  // rows a chunk, rounded up for the summed dimension
-  int64_t piece;       // of the vocabulary
-  int64_t pitch_d, ld_exps;
-  size_t factors, lse, said, most, stats, x, w, exps, g, gt, xt, sums, dw, bytes;
-};
 
 template <typename C>
 int64_t tiles_of(int64_t M, int64_t N) {
   return div_up(M, C::TM) * div_up(N, C::TN);
 }
-// 256 x 256 tiles where they give most compute units one.
-bool big(int64_t M, int64_t N, int cus) { return tiles_of<Big>(M, N) * 4 >= 3 * (int64_t)cus; }
 
-// d_hidden's summed dimension is shared out where it has few tiles.
-int split_of(int64_t D, int64_t chunk, int cus) {
-  if (big(D, chunk, cus)) return 1;
-  return (int)std::clamp<int64_t>(2 * cus / tiles_of<Small>(D, chunk), 1, kMaxSplit);
+enum Tiles { kBig, kMedium, kTiny };
+int wave_cols_of(Tiles t) { return t == kBig ? Big::WM : t == kMedium ? Medium::WM : Tiny::WM; }
+
+// The tiles of a product, and among how many workgroups each tile's summed
+// dimension is shared out (up to `most`; their sums are then joined): what takes
+// the least time by what a round of workgroups was measured to take, a step and
+// beside the steps, in us: 256 x 256 tiles 1.65 and 8 (8192 x 32768 x 4096: 67% of
+// the matrix units' time), 128 x 128, two a compute unit, 1.05 and 2, 64 x 64
+// 0.39 and 4 (1021 x 1001 x 50021).  So 512 x 131072 logits of 4096 take 440 us in
+// the largest tiles and 570 in the next, 1021 x 50021 of 1001 130 and 117,
+// 2000 x 512 of 256 in three parts 24 with 128 x 128 tiles and 12 with 64 x 64.
+struct Choice {
+  Tiles tiles;
+  int split;
+};
+Choice choose(int64_t M, int64_t N, int64_t steps, int terms, int cus, int most) {
+  struct {
+    int64_t tiles;
+    int slots;
+    double step, rest;
+  } const kinds[] = {{tiles_of<Big>(M, N), cus, 1.65, 8.0},
+                     {tiles_of<Medium>(M, N), 2 * cus, 1.05, 2.0},
+                     {tiles_of<Tiny>(M, N), cus, 0.39, 4.0}};
+  Choice best{kBig, 1};
+  double least = 1e300;
+  for (int t = 0; t < 3; ++t)
+    for (int split = 1; split <= most && split <= steps; split *= 2) {
+      const auto& k = kinds[t];
+      if (split > 1 && k.tiles * split > 2 * cus) break;
+      double us = (double)div_up(k.tiles * split, k.slots) *
+                  ((double)div_up(steps, split) * terms * k.step + k.rest);
+      if (split > 1) us += 4 + 2e-6 * (double)(M * N) * split;  // the sums written and read
+      if (us < least) {
+        least = us;
+        best = {(Tiles)t, split};
+      }
+    }
+  return best;
 }
+
+// What a call lays out in its workspace.
+struct Layout {
+  int parts;           // of an element
+  int64_t chunk, pad;  // rows a chunk, rounded up for the summed dimension
+  int64_t piece;       // of the vocabulary
+  int64_t pitch_d, ld_exps;
+  size_t lse, said, most, stats, x, w, wt, exps, g, gt, xt, sums, dw, bytes;
+};
 
 Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   Layout l{};
   l.parts = dtype == SGB_F32 ? 3 : 1;
   const int64_t V = p->V, D = p->D, exp_size = dtype == SGB_BF16 ? 2 : 4;
   l.pitch_d = up(D, kStep);
-  l.ld_exps = up(V, 256);
-  int64_t most = kStatBytes / (div_up(l.ld_exps, Small::WM) * 8);
+  l.ld_exps = up(V, 256);  // whole tiles
+  int64_t most = kStatBytes / (l.ld_exps / Tiny::WM * 8);
   if (gradient) most = std::min(most, kExpBytes / (l.ld_exps * exp_size));
   most = std::max<int64_t>(most / 256 * 256, 64);
   l.chunk = std::min(rows, most);
@@ -724,47 +895,49 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
     return here;
   };
   const int64_t part = 2ll * l.parts;
-  l.factors = take(4 * rows);
   l.lse = take(4 * rows);
   l.said = take(4 * rows);
   l.most = take(4);
-  l.stats = take(div_up(l.ld_exps, Small::WM) * 8 * l.chunk);
+  l.stats = take(l.ld_exps / Tiny::WM * 8 * l.chunk);
   l.x = take(l.chunk * l.pitch_d * part);
-  // a piece's weight rows, or their transpose
-  const int64_t all = std::max(l.ld_exps * l.pitch_d, D * l.ld_exps);
-  l.w = take(std::min(all, std::max(room, 256 * l.pitch_d)) * part);
+  // a piece's weight rows
+  l.w = take(std::min(l.ld_exps, std::max<int64_t>(256, room / l.pitch_d)) * l.pitch_d * part);
   if (gradient) {
+    l.wt = take(std::min(l.ld_exps, std::max<int64_t>(256, room / l.pitch_d)) * D * part);
     l.exps = take(l.chunk * l.ld_exps * exp_size);
-    const int64_t grads = std::min(l.pad * l.ld_exps, std::max(room, 256 * l.pad)) * part;
+    const int64_t grads = std::min(l.ld_exps * l.pad, std::max(room, 256 * l.pad)) * part;
     l.g = take(grads);
     l.gt = take(grads);
     l.xt = take(D * l.pad * part);
-    int64_t sums = 0;  // any fewer rows too
-    for (int64_t c = std::min<int64_t>(l.chunk, 64);; c = std::min(c + 64, l.chunk)) {
-      sums = std::max(sums, split_of(D, c, p->cus) * c);
-      if (c == l.chunk) break;
-    }
-    l.sums = take(sums * D * 4);
+    // a split's sums for any fewer rows too: at most 2 cus tiles
+    const int64_t shared = 2ll * p->cus * Big::TM * Big::TN / D + 1;
+    l.sums = take(std::max(l.chunk, std::min(kMaxSplit * l.chunk, shared)) * D * 4);
     if (rows > l.chunk && dtype != SGB_F32) l.dw = take(V * D * 4);
   }
   l.bytes = at;
   return l;
 }
 
-struct Operand {
-  const char* p;
-  int64_t ld, plane;  // bytes
-};
+template <typename E, int TERMS, int EPI, typename C>
+void launch(Product a, Product* b, hipStream_t s) {
+  const auto blocks = [](Product& p) {
+    p.tm = (int)div_up(p.M, C::TM);
+    p.tn = (int)div_up(p.N, C::TN);
+    return (unsigned)(div_up((int64_t)p.tm * p.tn * p.split, 8) * 8);
+  };
+  const unsigned first = blocks(a), second = b ? blocks(*b) : 0;
+  hipLaunchKernelGGL((k_product<E, TERMS, EPI, C>), dim3(first + second), dim3(kThreadsOf<C>), 0, s,
+                     a, b ? *b : a, (int)first);
+}
 
 template <typename E, int TERMS, int EPI>
-void product(Product& a, bool is_big, hipStream_t s) {
-  a.tm = (int)div_up(a.M, is_big ? Big::TM : Small::TM);
-  a.tn = (int)div_up(a.N, is_big ? Big::TN : Small::TN);
-  const dim3 grid((unsigned)(div_up((int64_t)a.tm * a.tn * a.split, 8) * 8));
-  if (is_big)
-    hipLaunchKernelGGL((k_product<E, TERMS, EPI, Big>), grid, dim3(kThreadsOf<Big>), 0, s, a);
+void product(const Product& a, Product* b, Tiles tiles, hipStream_t s) {
+  if (tiles == kBig)
+    launch<E, TERMS, EPI, Big>(a, b, s);
+  else if (tiles == kMedium)
+    launch<E, TERMS, EPI, Medium>(a, b, s);
   else
-    hipLaunchKernelGGL((k_product<E, TERMS, EPI, Small>), grid, dim3(kThreadsOf<Small>), 0, s, a);
+    launch<E, TERMS, EPI, Tiny>(a, b, s);
 }
 
 unsigned blocks(int64_t threads, int cus) {
@@ -772,6 +945,26 @@ unsigned blocks(int64_t threads, int cus) {
 }
 
 enum Way { kForward, kBackward, kBoth };
+
+struct Operand {
+  const char* p;
+  int64_t ld, plane;  // bytes
+};
+
+template <typename T>
+struct Copies {  // asked for, to be launched together
+  Copy<T> c[2];
+  int n = 0;
+  static unsigned tiles(const Copy<T>& c) {
+    return (unsigned)(div_up(c.rows, kTile) * div_up(c.D, kTile));
+  }
+  void launch(hipStream_t s) {
+    if (n == 0) return;
+    const unsigned first = tiles(c[0]), second = n > 1 ? tiles(c[1]) : 0;
+    hipLaunchKernelGGL(k_copy<T>, dim3(first + second), dim3(256), 0, s, c[0], c[n - 1], first);
+    n = 0;
+  }
+};
 
 template <typename T>
 void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const Layout& l, char* ws,
@@ -782,46 +975,63 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
   constexpr float kBy = __is_same(T, f16_t) ? kUp : 1.f;
   const int64_t R = q->rows, V = p->V;
   const int D = p->D;
-  Header* hdr = reinterpret_cast<Header*>(ws);
-  const uint32_t epoch = next_epoch();
-  const auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
-  E* const xc = reinterpret_cast<E*>(ws + l.x);
-  E* const wc = reinterpret_cast<E*>(ws + l.w);
-  float *factors = at(l.factors), *most = at(l.most), *said = at(l.said);
-  const float* lse_in = q->lse;
-  float* lse_out = q->lse ? q->lse : at(l.lse);
-  const float* lse = way == kBackward ? lse_in : lse_out;
-  const T* hidden = static_cast<const T*>(q->hidden);
-  const T* weight = static_cast<const T*>(q->weight);
   const bool grad = way != kForward;
+  const auto floats = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  const auto elems = [&](size_t o) { return reinterpret_cast<E*>(ws + o); };
+  float* most = __is_same(T, f16_t) && grad && q->d_weight ? floats(l.most) : nullptr;
+  float* lse = q->lse ? q->lse : floats(l.lse);
+  const float* above = way == kBackward ? q->grad_loss : nullptr;
+  const T* weight = static_cast<const T*>(q->weight);
+  const uint32_t epoch = next_epoch();
+  const auto rows_at = [&](int64_t r) {
+    return Rows{q->labels + r, q->row_weights ? q->row_weights + r : nullptr,
+                above ? above + r : nullptr, V};
+  };
+  if (most) hipLaunchKernelGGL(k_most, dim3(1), dim3(1024), 0, s, rows_at(0), R, most);
 
-  if (grad)
-    hipLaunchKernelGGL(k_factors, dim3(1), dim3(1024), 0, s, q->labels, q->row_weights,
-                       way == kBackward ? q->grad_loss : nullptr, R, V, factors, most, hdr, epoch);
-  // Rows as the product reads them: whole 128-byte lines, 16-byte aligned.
+  // Rows as the product reads them: whole 128-byte lines, 16-byte aligned, a
+  // tile's within 32 bits.
   const auto fits = [&](const void* a, int64_t stride, int64_t rows) {
-    return sizeof(T) == 2 && D % kStep == 0 && aligned(a, 16) && (rows < 2 || stride % 8 == 0);
+    return sizeof(T) == 2 && D % kStep == 0 && aligned(a, 16) &&
+           (rows < 2 || (stride % 8 == 0 && stride < (1 << 22)));
   };
-  const auto rows_of = [&](const T* src, int64_t stride, int64_t n, E* to) -> Operand {
-    if (fits(src, stride, n)) return {reinterpret_cast<const char*>(src), stride * 2, 0};
-    const int64_t plane = n * l.pitch_d;
-    hipLaunchKernelGGL(k_rows<T>, dim3(blocks(plane / 8, p->cus)), dim3(256), 0, s, src, stride, n, D,
-                       to, l.pitch_d, plane);
-    return {reinterpret_cast<const char*>(to), l.pitch_d * 2, plane * 2};
-  };
-  const auto columns_of = [&](const T* src, int64_t stride, int64_t n, const float* only,
-                              E* to) -> Operand {
-    const int64_t pitch = up(n, kStep), plane = D * pitch;
-    const unsigned grid = (unsigned)(pitch / kTile * div_up(D, kTile));
-    hipLaunchKernelGGL(k_transpose<T>, dim3(grid), dim3(256), 0, s, src, stride, n, D, only, to, pitch,
-                       plane);
-    return {reinterpret_cast<const char*>(to), pitch * 2, plane * 2};
+  Copies<T> copies;
+  // Asks for a copy of rows (to) and of columns (to_t), where they are wanted.
+  const auto operands = [&](const T* src, int64_t stride, int64_t n, const Rows* only, E* to, E* to_t,
+                            Operand* rows, Operand* columns) {
+    Copy<T> c{src, stride, n, D};
+    c.pitch = l.pitch_d;
+    c.plane = n * c.pitch;
+    c.pitch_t = up(n, kStep);
+    c.plane_t = D * c.pitch_t;
+    if (only) {
+      c.only = true;
+      c.count = *only;
+    }
+    if (rows) {
+      if (fits(src, stride, n)) {
+        *rows = {reinterpret_cast<const char*>(src), stride * 2, 0};
+      } else {
+        c.to = to;
+        *rows = {reinterpret_cast<const char*>(to), c.pitch * 2, c.plane * 2};
+      }
+    }
+    if (columns) {
+      c.to_t = to_t;
+      *columns = {reinterpret_cast<const char*>(to_t), c.pitch_t * 2, c.plane_t * 2};
+    }
+    if (c.to || c.to_t) copies.c[copies.n++] = c;
   };
 
+  // the logits by pieces only where the weight's rows have to be copied
+  const int64_t logits_piece = fits(weight, q->weight_stride, V) ? V : l.piece;
+  const bool one_piece = l.piece >= V;
   for (int64_t r0 = 0; r0 < R; r0 += l.chunk) {
     const int64_t n = std::min(l.chunk, R - r0);
-    const T* x = hidden + r0 * q->hidden_stride;
-    const Operand xo = rows_of(x, q->hidden_stride, n, xc);
+    const Rows rows = rows_at(r0);
+    Operand xo, xt, wo, wt;
+    operands(static_cast<const T*>(q->hidden) + r0 * q->hidden_stride, q->hidden_stride, n, &rows,
+             elems(l.x), elems(l.xt), &xo, grad && q->d_weight ? &xt : nullptr);
     Product a{};
     a.b = xo.p;
     a.ldb = xo.ld;
@@ -829,118 +1039,144 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     a.N = a.tokens = n;
     a.steps = (int)(l.pitch_d / kStep);
     a.split = 1;
+    a.rows = rows;
     a.stats = reinterpret_cast<float2*>(ws + l.stats);
-    a.labels = q->labels + r0;
-    a.lse = lse ? lse + r0 : nullptr;
-    a.said = said + r0;
+    a.lse = lse + r0;
+    a.said = floats(l.said) + r0;
     a.exps = ws + l.exps;
     a.ld_exps = l.ld_exps;
-    a.V = V;
-    // the waves' width has to be one for all pieces
-    const bool whole = fits(weight, q->weight_stride, V);
-    const int64_t stride_v = whole ? V : l.piece;
-    const bool is_big = big(std::min(stride_v, V), n, p->cus);
-    const int wave_cols = is_big ? Big::WM : Small::WM;
-    for (int64_t v0 = 0; v0 < V; v0 += stride_v) {
-      const int64_t width = std::min(stride_v, V - v0);
-      const Operand wo = rows_of(weight + v0 * q->weight_stride, q->weight_stride, width, wc);
+    // (one kind of tile for all pieces: they share the rows of sums)
+    const Tiles tiles = choose(std::min(logits_piece, V), n, a.steps, TERMS, p->cus, 1).tiles;
+    for (int64_t v0 = 0; v0 < V; v0 += logits_piece) {
+      const int64_t width = std::min(logits_piece, V - v0);
+      operands(weight + v0 * q->weight_stride, q->weight_stride, width, nullptr, elems(l.w),
+               elems(l.wt), &wo, grad && q->d_hidden && one_piece ? &wt : nullptr);
+      copies.launch(s);
       a.a = wo.p;
       a.lda = wo.ld;
       a.plane_a = wo.plane;
       a.M = width;
       a.v0 = v0;
       if (way == kForward)
-        product<E, TERMS, kSums>(a, is_big, s);
+        product<E, TERMS, kSums>(a, nullptr, tiles, s);
       else if (way == kBoth)
-        product<E, TERMS, kExps>(a, is_big, s);
+        product<E, TERMS, kExps>(a, nullptr, tiles, s);
       else
-        product<E, TERMS, kProbs>(a, is_big, s);
+        product<E, TERMS, kProbs>(a, nullptr, tiles, s);
     }
-    if (way != kBackward)
-      hipLaunchKernelGGL(k_lse, dim3((unsigned)div_up(n, 16)), dim3(256), 0, s, a.stats,
-                         (int)div_up(V, wave_cols), n, a.labels,
-                         q->row_weights ? q->row_weights + r0 : nullptr, a.said, V, q->loss + r0,
-                         lse_out + r0, hdr, epoch);
-    if (!grad) continue;
+    Loss loss{};
+    loss.stats = a.stats;
+    loss.parts = (int)div_up(V, wave_cols_of(tiles));
+    loss.tokens = n;
+    loss.rows = rows;
+    loss.said = a.said;
+    loss.loss = q->loss ? q->loss + r0 : nullptr;
+    loss.lse = lse + r0;
+    loss.hdr = reinterpret_cast<Header*>(ws);
+    loss.epoch = epoch;
+    const bool gradients = grad && (q->d_hidden || q->d_weight);
+    const bool sum_later = way == kBoth && gradients && one_piece && loss.parts <= kFewParts;
+    if (way != kBackward && !sum_later)
+      hipLaunchKernelGGL(k_lse, dim3((unsigned)div_up(n, 16)), dim3(256), 0, s, loss);
+    if (!gradients) continue;
 
-    Operand xt{};
-    if (q->d_weight) xt = columns_of(x, q->hidden_stride, n, factors + r0, reinterpret_cast<E*>(ws + l.xt));
-    const int split = split_of(D, n, p->cus);
+    // (of the first piece, the longest, which writes every part's sums)
+    const Choice for_h = choose(D, n, div_up(std::min(l.piece, V), kStep), TERMS, p->cus, kMaxSplit);
+    const int split = for_h.split;
     for (int64_t v0 = 0; v0 < V; v0 += l.piece) {
       const int64_t width = std::min(l.piece, V - v0);
       Grad g{};
       g.exps = a.exps;
       g.ld_exps = l.ld_exps;
-      g.tokens = n;
-      g.stats = way == kBoth ? a.stats : nullptr;
-      g.wave_cols = wave_cols;
+      g.wave_cols = way == kBoth ? wave_cols_of(tiles) : 0;
+      g.rows = loss;
       g.lse = lse + r0;
-      g.labels = a.labels;
-      g.factors = factors + r0;
       g.most = most;
       g.v0 = v0;
       g.width = width;
-      g.V = V;
       g.pitch = up(width, kStep);
       g.plane = n * g.pitch;
       g.pitch_t = up(n, kStep);
       g.plane_t = width * g.pitch_t;
       g.g = q->d_hidden ? ws + l.g : nullptr;
       g.gt = q->d_weight ? ws + l.gt : nullptr;
-      hipLaunchKernelGGL((k_grad<T, X>), dim3((unsigned)(g.pitch / kTile * (g.pitch_t / kTile))),
-                         dim3(256), 0, s, g);
+      const dim3 grid((unsigned)(g.pitch / kTile * (g.pitch_t / kTile)));
+      if (sum_later)
+        hipLaunchKernelGGL((k_grad<T, X, true>), grid, dim3(256), 0, s, g);
+      else
+        hipLaunchKernelGGL((k_grad<T, X, false>), grid, dim3(256), 0, s, g);
+      Product h{}, w{};
       if (q->d_hidden) {
-        const Operand wt = columns_of(weight + v0 * q->weight_stride, q->weight_stride, width, nullptr, wc);
-        Product b{};
-        b.a = wt.p;
-        b.lda = wt.ld;
-        b.plane_a = wt.plane;
-        b.b = static_cast<const char*>(g.g);
-        b.ldb = g.pitch * 2;
-        b.plane_b = g.plane * 2;
-        b.M = D;
-        b.N = n;
-        b.steps = (int)(g.pitch / kStep);
-        b.split = split;
-        b.sums = at(l.sums);
-        b.add = v0 > 0;
-        product<E, TERMS, kAdd>(b, big(D, n, p->cus), s);
+        if (!one_piece) {
+          operands(weight + v0 * q->weight_stride, q->weight_stride, width, nullptr, nullptr,
+                   elems(l.wt), nullptr, &wt);
+          copies.launch(s);
+        }
+        h.a = wt.p;
+        h.lda = wt.ld;
+        h.plane_a = wt.plane;
+        h.b = static_cast<const char*>(g.g);
+        h.ldb = g.pitch * 2;
+        h.plane_b = g.plane * 2;
+        h.M = D;
+        h.N = n;
+        h.steps = (int)(g.pitch / kStep);
+        h.split = std::min(split, h.steps);
+        if (split == 1 && v0 + width == V) {
+          h.rows = rows;
+          h.by_row = true;
+          h.scale = q->grad_scale / kBy;
+          h.add_from = v0 > 0 ? floats(l.sums) : nullptr;
+          h.out = static_cast<T*>(q->d_hidden) + r0 * q->d_hidden_stride;
+          h.ldo = q->d_hidden_stride;
+          h.out_dtype = q->dtype;
+        } else {
+          h.sums = floats(l.sums);
+          h.add = v0 > 0;
+        }
       }
+      Tiles tiles_w = kBig;
       if (q->d_weight) {
         const bool first = r0 == 0, last = r0 + n == R;
         const bool direct = (first && last) || q->d_weight_dtype == SGB_F32;
-        Product b{};
-        b.a = xt.p;
-        b.lda = xt.ld;
-        b.plane_a = xt.plane;
-        b.b = static_cast<const char*>(g.gt);
-        b.ldb = g.pitch_t * 2;
-        b.plane_b = g.plane_t * 2;
-        b.M = D;
-        b.N = width;
-        b.steps = (int)(g.pitch_t / kStep);
-        b.split = 1;
-        b.most = most;
-        b.scale = q->grad_scale / kBy;
+        tiles_w = choose(D, width, g.pitch_t / kStep, TERMS, p->cus, 1).tiles;
+        w.a = xt.p;
+        w.lda = xt.ld;
+        w.plane_a = xt.plane;
+        w.b = static_cast<const char*>(g.gt);
+        w.ldb = g.pitch_t * 2;
+        w.plane_b = g.plane_t * 2;
+        w.M = D;
+        w.N = width;
+        w.steps = (int)(g.pitch_t / kStep);
+        w.split = 1;
+        w.most = most;
+        w.scale = q->grad_scale / kBy;
         if (direct || last) {
-          const size_t e = elem_size(q->d_weight_dtype);
-          b.out = static_cast<char*>(q->d_weight) + v0 * q->d_weight_stride * e;
-          b.ldo = q->d_weight_stride;
-          b.out_dtype = q->d_weight_dtype;
-          b.add = q->accumulate || (direct && !first);
-          b.add_from = direct ? nullptr : at(l.dw) + v0 * D;
+          w.out = static_cast<char*>(q->d_weight) +
+                  v0 * q->d_weight_stride * elem_size(q->d_weight_dtype);
+          w.ldo = q->d_weight_stride;
+          w.out_dtype = q->d_weight_dtype;
+          w.add = q->accumulate || (direct && !first);
+          w.add_from = direct ? nullptr : floats(l.dw) + v0 * D;
         } else {
-          b.out = at(l.dw) + v0 * D;
-          b.ldo = D;
-          b.out_dtype = SGB_F32;
-          b.add = !first;
+          w.out = floats(l.dw) + v0 * D;
+          w.ldo = D;
+          w.out_dtype = SGB_F32;
+          w.add = !first;
         }
-        product<E, TERMS, kOut>(b, big(D, width, p->cus), s);
+      }
+      // two products that leave compute units idle run side by side
+      if (q->d_hidden && q->d_weight && for_h.tiles == kTiny && tiles_w == kTiny) {
+        product<E, TERMS, kGrads>(h, &w, kTiny, s);
+      } else {
+        if (q->d_hidden) product<E, TERMS, kGrads>(h, nullptr, for_h.tiles, s);
+        if (q->d_weight) product<E, TERMS, kGrads>(w, nullptr, tiles_w, s);
       }
     }
-    if (q->d_hidden)
-      hipLaunchKernelGGL(k_join<T>, dim3(blocks(n * div_up(D, 8), p->cus)), dim3(256), 0, s, at(l.sums),
-                         split, n, D, factors + r0, q->grad_scale / kBy,
+    if (q->d_hidden && split > 1)
+      hipLaunchKernelGGL(k_join<T>, dim3(blocks(n * div_up(D, 8), p->cus)), dim3(256), 0, s,
+                         floats(l.sums), split, n, D, rows, q->grad_scale / kBy,
                          static_cast<T*>(q->d_hidden) + r0 * q->d_hidden_stride, q->d_hidden_stride);
   }
 }
