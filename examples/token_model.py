@@ -6,8 +6,11 @@ Token rows come from the embedding forward (one row a token) and go through one
 block, x_out = x + gate * post(mlp(x)), y = pre(x_out); the logits y @ head.T
 are trained on a teacher's top logits and the tokens that follow, and the
 gradient goes back through the block norms into the embedding rows, which
-sgb's backward updates in place.  Then tokens are generated under a
-grammar mask with a presence penalty.  Matrix products are torch's.
+sgb's backward updates in place.  Before that the model is trained on the tokens
+that follow alone, its embedding rows under dropout, with the loss and gradients
+of the head's product taken in one call.  Then tokens are generated under a
+grammar mask with a presence penalty, also with the last norm's output in 8 bits.
+The other matrix products are torch's.
 """
 import argparse
 import os
@@ -37,6 +40,9 @@ class TokenModel:
         self.norm = lm.BlockNorm(D, post="rms", pre="rms", post_weight=ones[0], pre_weight=ones[1])
         self.distill = lm.TopkDistill(vocab, K, kd_weight=0.7, ce_weight=0.3)
         self.penalty = lm.LogitsPenalty(vocab)
+        self.dropout, self.ce = lm.Dropout(0.1), lm.VocabCrossEntropy(D, vocab)
+        self.block = lm.BlockNorm(D, post="rms", pre="none", post_weight=ones[0])
+        self.quant = lm.QuantNorm(D, weight=ones[1], form="int8")
         self.plan = sgb.Plan([0, vocab], [0, D], "none")
         new = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
         self.x, self.x_out, self.y = new(rows, D), new(rows, D), new(rows, D)
@@ -44,19 +50,41 @@ class TokenModel:
         self.stats, self.loss = new(rows, 4), new(rows)
         self.d_logits = new(rows, vocab)
         self.d_gate, self.d_norm = new(1, D), new(2, D)
+        self.dy, self.d_head = new(rows, D), new(vocab, D)
+        self.codes = torch.empty(rows, D, dtype=torch.int8, device="cuda")
+        self.scales = new(rows, 1)
         self.none = torch.zeros(rows, D, device="cuda")      # nothing reads x_out but the norm
         self.ws = (self.plan.workspace(rows, 0), self.norm.workspace(rows),
-                   self.distill.workspace(rows), self.penalty.workspace(rows))
+                   self.distill.workspace(rows), self.penalty.workspace(rows),
+                   self.ce.workspace(rows, torch.float32))
 
-    def logits(self, tokens):
-        """Of `rows` or fewer tokens, each alone."""
+    def block_output(self, tokens, drop=None):
+        """x and h of `rows` or fewer tokens, each alone; drop: seed and step of
+        the embedding rows' dropout."""
         n = tokens.numel()
         self.plan.forward(tokens, None, 0, None, self.table, self.x[:n], self.ws[0])
+        if drop is not None:
+            self.dropout.forward(self.x[:n], self.x[:n], *drop)
         self.a = torch.tanh(self.x[:n] @ self.w1.t())
         self.h = self.a @ self.w2.t()
+        return n
+
+    def hidden(self, tokens, drop=None):
+        """What the head is multiplied with."""
+        n = self.block_output(tokens, drop)
         self.norm.forward(self.x[:n], self.h, self.x_out[:n], self.y[:n], gate=self.gate,
                           rows_per_gate=n, stats=self.stats[:n])
-        return self.y[:n] @ self.head.t()
+        return self.y[:n]
+
+    def logits(self, tokens):
+        return self.hidden(tokens) @ self.head.t()
+
+    def logits_of_codes(self, tokens):
+        """The same with the last norm's output in 8 bits, a scale a row."""
+        n = self.block_output(tokens)
+        self.block.forward(self.x[:n], self.h, self.x_out[:n], gate=self.gate, rows_per_gate=n)
+        self.quant.forward(self.x_out[:n], self.codes[:n], self.scales[:n])
+        return self.codes[:n].float() @ self.head.t() * self.scales[:n]
 
     def step(self, tokens, labels, ids, values, lse, lr):
         """One training step on `rows` tokens; returns the mean loss."""
@@ -64,7 +92,19 @@ class TokenModel:
         self.distill.loss_grad(logits, ids, values, self.loss, self.d_logits,
                                grad_scale=1.0 / self.rows, teacher_lse=lse, labels=labels,
                                workspace=self.ws[2])
-        dy, d_head = self.d_logits @ self.head, self.d_logits.t() @ self.y
+        self.update(tokens, self.d_logits @ self.head, self.d_logits.t() @ self.y, lr)
+        return self.loss.mean()
+
+    def step_on_labels(self, tokens, labels, lr, step, seed=0):
+        """One training step on the tokens that follow; returns the mean loss."""
+        y = self.hidden(tokens, (seed, step))
+        self.ce.loss_grad(y, self.head, labels, self.loss, self.dy, self.d_head,
+                          grad_scale=1.0 / self.rows, workspace=self.ws[4])
+        self.update(tokens, self.dy, self.d_head, lr, (seed, step))
+        return self.loss.mean()
+
+    def update(self, tokens, dy, d_head, lr, drop=None):
+        """Back from the gradients of y and of the head; every parameter moves."""
         self.norm.backward(self.none, dy, self.x_out, self.h, self.stats, self.dx, self.dh,
                            gate=self.gate, rows_per_gate=self.rows, d_gate=self.d_gate,
                            d_post_weight=self.d_norm[0], d_pre_weight=self.d_norm[1],
@@ -72,23 +112,25 @@ class TokenModel:
         da = (self.dh @ self.w2) * (1 - self.a * self.a)
         d_w2, d_w1 = self.dh.t() @ self.a, da.t() @ self.x
         dx = self.dx + da @ self.w1
+        if drop is not None:
+            self.dropout.backward(dx, dx, *drop)
         for w, d in ((self.w1, d_w1), (self.w2, d_w2), (self.head, d_head), (self.gate, self.d_gate),
                      (self.norm.post_weight, self.d_norm[0]), (self.norm.pre_weight, self.d_norm[1])):
             w.sub_(d, alpha=lr)
         self.plan.backward(dx, tokens, None, 0, None, "sgd", weights=self.table, lr=lr,
                            workspace=self.ws[0])
-        return self.loss.mean()
 
-    def generate(self, first, count, mask):
+    def generate(self, first, count, mask, codes=False):
         """`count` tokens after each of `first`, the likeliest that the grammar
-        row `mask` (packed bits) allows, with a heavy presence penalty."""
+        row `mask` (packed bits) allows, with a heavy presence penalty; codes:
+        from logits of 8-bit codes."""
         n = first.numel()
         seq = torch.zeros(n, count + 1, dtype=torch.int32, device="cuda")
         seq[:, 0] = first
         prompt = torch.ones(n, dtype=torch.int32, device="cuda")
         which, heavy = torch.zeros_like(prompt), torch.full((n,), 1e4, device="cuda")
         for i in range(1, count + 1):
-            logits = self.logits(seq[:, i - 1].long())
+            logits = (self.logits_of_codes if codes else self.logits)(seq[:, i - 1].long())
             self.penalty.apply(logits, logits, tokens=seq, prompt_lens=prompt,
                                lens=torch.full_like(prompt, i), presence=heavy, mask=mask,
                                mask_index=which, workspace=self.ws[3])
@@ -96,20 +138,24 @@ class TokenModel:
         return seq
 
 
-def train(steps=60, seed=0):
-    """Returns the model and its losses.  The teacher is a fixed table of next-token logits."""
+def train(steps=60, seed=0, on_labels=0):
+    """Returns the model and its losses, after `on_labels` steps on the following
+    tokens alone.  The teacher is a fixed table of next-token logits."""
     m = TokenModel(seed=seed)
     teacher = m.rand(m.V, m.V, std=2.0)
     values, ids = teacher.topk(m.K, dim=1)
     lse = torch.logsumexp(teacher.double(), 1).float()
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
     losses = []
-    for _ in range(steps):
+    for i in range(on_labels + steps):
         # token frequencies fall off as in text: rows repeat within a batch
         u = torch.rand(m.rows, generator=g, device="cuda")
         tokens = (m.V ** u - 1).long().clamp_(max=m.V - 1)
         labels = ids[tokens, torch.randint(0, m.K, (m.rows,), generator=g, device="cuda")]
-        losses.append(m.step(tokens, labels, ids[tokens], values[tokens], lse[tokens], lr=2.0))
+        if i < on_labels:
+            m.step_on_labels(tokens, labels, 2.0, i, seed)
+        else:
+            losses.append(m.step(tokens, labels, ids[tokens], values[tokens], lse[tokens], lr=2.0))
     return m, torch.stack(losses).tolist()
 
 
@@ -121,10 +167,12 @@ def even_tokens(vocab):
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=60)
+    ap.add_argument("--on-labels", type=int, default=20)
     a = ap.parse_args()
-    m, losses = train(a.steps)
+    m, losses = train(a.steps, on_labels=a.on_labels)
     print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} in {a.steps} steps")
-    print(m.generate(torch.arange(4, device="cuda").int(), 8, even_tokens(m.V)).tolist())
+    for codes in (False, True):
+        print(m.generate(torch.arange(4, device="cuda").int(), 8, even_tokens(m.V), codes).tolist())
 
 
 if __name__ == "__main__":

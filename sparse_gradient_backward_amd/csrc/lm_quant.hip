@@ -113,8 +113,8 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_quant(Args a) {
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      v[i] = i < n ? v[i] * rs * w[i] : 0.f;
-      most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+      const float u = i < n ? v[i] * rs * w[i] : 0.f;
+      most = max(most, __float_as_uint(u) & 0x7fffffffu);
     }
     if (a.in_group) {
       most = fold_most(most, a.in_group);
@@ -130,13 +130,14 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_quant(Args a) {
     phase ^= 1;
     float scale = __uint_as_float(most) / kMost;
     if (scale < 0x1p-126f) scale = 0.f;
-    // A quotient of the rounded scale, each correctly rounded: a product with a
-    // reciprocal moves codes on the border between two.
+    // The codes come from the sums' fp64 products over the fp32 largest: every
+    // rounding on the way to them moves a few codes on the border between two.
     const bool fine = scale > 0.f && scale < INFINITY;  // nor NaN
+    const double by = fine ? (double)rs * (kMost / (double)__uint_as_float(most)) : 0.0;
     float c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      c[i] = fine ? fminf(fmaxf(v[i] / scale, -kMost), kMost) : 0.f;
+      c[i] = fine ? fminf(fmaxf((float)((double)v[i] * (double)w[i] * by), -kMost), kMost) : 0.f;
     if (!mine || n <= 0) continue;
     const int lanes = a.in_group ? a.in_group : a.tpr;
     const int in_row = t % a.tpr;
