@@ -38,48 +38,76 @@ struct Args {
 
 // Largest of x over groups of `width` lanes (4, 8, .. 64): one that is no number
 // wins.  Magnitudes as words compare like their values, and NaN above all.
-__device__ __forceinline__ uint32_t fold_most(uint32_t x, int width) {
+__device__ __forceinline__ float fold_most(float v, int width) {
   const auto f = [](float a, float b) {
     return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
   };
-  float v = __uint_as_float(x);
   if (width == 4) {
     v = f(v, dpp<0xB1>(v));
-    v = f(v, dpp<0x4E>(v));
-  } else {
-    v = wave_fold(v, width, f);
+    return f(v, dpp<0x4E>(v));
   }
-  return __float_as_uint(v);
+  return wave_fold(v, width, f);
 }
 
-// WAVES: a row is a wave's or less (0), or whole waves' (their number).
-template <typename T, typename U, int CODE, bool WIDE, bool TINY>
-__global__ __launch_bounds__(WIDE ? 1024 : 256) void k_quant(Args a) {
-  __shared__ float sums[2][kMaxWaves];
-  __shared__ uint32_t mosts[2][kMaxWaves];
-  constexpr float kMost = CODE == SGB_CODE_INT8 ? 127.f : 448.f;
+// Codes are p * by, p = v * weight and by = M / (the largest p): 1 / rms cancels.
+// Every rounding on the way moves a few codes of those on the border between
+// two, so p keeps its rest, by is two floats, and only their sum is rounded.
+struct Factor {
+  float hi, lo;
+  bool on;
+};
+__device__ __forceinline__ Factor factor_of(float most_p, float scale, float M) {
+  Factor f{0.f, 0.f, scale > 0.f && scale < INFINITY};  // nor NaN
+  if (most_p > 0x1p-90f && most_p < 0x1p90f) {
+    float r = __builtin_amdgcn_rcpf(most_p);
+    r = fmaf(r, fmaf(-most_p, r, 1.f), r);
+    f.hi = M * r;
+    f.lo = fmaf(-most_p, f.hi, M) * r;
+  } else if (f.on) {
+    const double by = (double)M / (double)most_p;
+    f.hi = (float)by;
+    f.lo = (float)(by - (double)f.hi);
+  }
+  return f;
+}
+
+// WIDE: a row is one or more whole waves'.  K: vectors of eight a lane.  RES:
+// there is a residual.
+template <typename T, typename U, int CODE, bool WIDE, int K, bool RES, bool TINY>
+__global__ __launch_bounds__(WIDE ? 512 : 256) void k_quant(Args a) {
+  __shared__ float2 parts[2][kMaxWaves];  // a wave's sum of squares, its largest p
+  constexpr float M = CODE == SGB_CODE_INT8 ? 127.f : 448.f;
   const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
   const int teams = (int)blockDim.x / a.tpr, nw = WIDE ? a.tpr >> 6 : 1;
   const int team = WIDE ? __builtin_amdgcn_readfirstlane(t / a.tpr) : t / a.tpr;
-  const int col = (t % a.tpr) * 8, n = max(0, min(8, a.D - col));
-  const int first = wave / nw * nw;
-
-  RawAs wr = ask8_as<TINY>(a.weight, a.weight_dtype, col, a.D);
-  float w[8];
-  have8_as<TINY>(wr, a.weight, a.weight_dtype, col, n, 1.f, w);
+  const int in_row = t % a.tpr, first = wave / nw * nw;
+  int col[K], n[K];
+  float w[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    col[k] = (in_row + k * a.tpr) * 8;
+    n[k] = max(0, min(8, a.D - col[k]));
+    const RawAs wr = ask8_as<TINY>(a.weight, a.weight_dtype, col[k], a.D);
+    have8_as<TINY>(wr, a.weight, a.weight_dtype, col[k], n[k], 1.f, w[k]);
+  }
 
   const int64_t step = (int64_t)gridDim.x * teams;
   int64_t r = (int64_t)blockIdx.x * teams + team;
-  Raw8<T> h;
-  Raw8<U> x;
+  Raw8<T> h[K];
+  Raw8<U> x[K];
   const auto ask = [&](int64_t row) {
     const int64_t at = min(row, a.rows - 1);  // past the last: loaded, not used
-    if (TINY) {
-      h = load8(static_cast<const T*>(a.h) + at * a.sh + col, n);
-      x = load8(static_cast<const U*>(a.x) + at * a.sx + col, a.x ? n : 0);
-    } else {
-      h = ask8(static_cast<const T*>(a.h) + at * a.sh, (uint32_t)col, (uint32_t)a.D);
-      x = ask8(a.x ? static_cast<const U*>(a.x) + at * a.sx : nullptr, (uint32_t)col, (uint32_t)a.D);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const T* ph = static_cast<const T*>(a.h) + at * a.sh;
+      const U* px = static_cast<const U*>(a.x) + at * a.sx;
+      if (TINY) {
+        h[k] = load8(ph + col[k], n[k]);
+        if (RES) x[k] = load8(px + col[k], n[k]);
+      } else {
+        h[k] = ask8(ph, (uint32_t)col[k], (uint32_t)a.D);
+        if (RES) x[k] = ask8(px, (uint32_t)col[k], (uint32_t)a.D);
+      }
     }
   };
   ask(r);
@@ -88,98 +116,123 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_quant(Args a) {
   const int64_t turns = (a.rows + step - 1) / step;
   for (int64_t turn = 0; turn < turns; ++turn, r += step) {
     const bool mine = r < a.rows;
-    if (!TINY) {
-      have8(h, n);
-      have8(x, n);
-    }
-    float v[8], y[8];
-    widen8(h, v);
-    widen8(x, y);
+    float v[K][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += y[i];
-    if (turn + 1 < turns) ask(r + step);
-    if (mine && a.x_out && n > 0) store8(static_cast<U*>(a.x_out) + r * a.sxo + col, v, n);
-    float s = 0.f;
+    for (int k = 0; k < K; ++k) {
+      if (!TINY) have8(h[k], n[k]);
+      widen8(h[k], v[k]);
+      if (RES) {
+        float y[8];
+        if (!TINY) have8(x[k], n[k]);
+        widen8(x[k], y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);  // columns past the row are zeros
-    s = wave_add(s, WIDE ? 64 : a.tpr);
-    if (WIDE) {
-      if (lane == 0) sums[phase][wave] = s;
-      __syncthreads();
-      s = wave_add(lane < nw ? sums[phase][first + lane] : 0.f, 16);
-      s = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(s)));
-    }
-    const float rs = 1.0f / sqrtf(fmaf(s, a.inv_d, a.eps));
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float u = i < n ? v[i] * rs * w[i] : 0.f;
-      most = max(most, __float_as_uint(u) & 0x7fffffffu);
-    }
-    if (a.in_group) {
-      most = fold_most(most, a.in_group);
-    } else {
-      most = fold_most(most, WIDE ? 64 : a.tpr);
-      if (WIDE) {
-        if (lane == 0) mosts[phase][wave] = most;
-        __syncthreads();
-        most = fold_most(lane < nw ? mosts[phase][first + lane] : 0u, 16);
-        most = (uint32_t)__builtin_amdgcn_readfirstlane((int)most);
+        for (int i = 0; i < 8; ++i) v[k][i] += y[i];
       }
     }
-    phase ^= 1;
-    float scale = __uint_as_float(most) / kMost;
-    if (scale < 0x1p-126f) scale = 0.f;
-    // The codes come from the sums' fp64 products over the fp32 largest: every
-    // rounding on the way to them moves a few codes on the border between two.
-    const bool fine = scale > 0.f && scale < INFINITY;  // nor NaN
-    const double by = fine ? (double)rs * (kMost / (double)__uint_as_float(most)) : 0.0;
-    float c[8];
+    if (turn + 1 < turns) ask(r + step);
+    float s = 0.f, most[K], all = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      c[i] = fine ? fminf(fmaxf((float)((double)v[i] * (double)w[i] * by), -kMost), kMost) : 0.f;
-    if (!mine || n <= 0) continue;
-    const int lanes = a.in_group ? a.in_group : a.tpr;
-    const int in_row = t % a.tpr;
-    if (in_row % lanes == 0) a.scales[r * a.ss + in_row / lanes] = scale;
-    if (a.stats && in_row == 0) {
+    for (int k = 0; k < K; ++k) {
+      if (mine && a.x_out && n[k] > 0) store8(static_cast<U*>(a.x_out) + r * a.sxo + col[k], v[k], n[k]);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // (columns past the row are zeros, and so is their weight)
+        s = fmaf(v[k][i], v[k][i], s);
+        top = max(top, __float_as_uint(v[k][i] * w[k][i]) & 0x7fffffffu);
+      }
+      most[k] = __uint_as_float(top);
+      all = __uint_as_float(max(__float_as_uint(all), top));
+    }
+    // one exchange for the row's squares and its largest
+    s = wave_add(s, WIDE ? 64 : a.tpr);
+    if (a.in_group) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) most[k] = fold_most(most[k], a.in_group);
+    } else {
+      all = fold_most(all, WIDE ? 64 : a.tpr);
+    }
+    if (WIDE && nw > 1) {
+      if (lane == 0) parts[phase][wave] = make_float2(s, all);
+      __syncthreads();
+      const float2 part = lane < nw ? parts[phase][first + lane] : make_float2(0.f, 0.f);
+      phase ^= 1;
+      s = wave_add(part.x, 16);
+      s = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(s)));
+      if (!a.in_group) {
+        all = fold_most(part.y, 16);
+        all = __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(all)));
+      }
+    }
+    const float rs = 1.0f / sqrtf(fmaf(s, a.inv_d, a.eps));
+    if (mine && a.stats && in_row == 0) {
       typedef float F4 __attribute__((ext_vector_type(4)));
       *reinterpret_cast<F4*>(a.stats + 4 * r) = F4{0.f, 1.f, 0.f, rs};
     }
-    uint32_t b[2] = {0, 0};
-    if (CODE == SGB_CODE_INT8) {
+    Factor by;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        b[i >> 2] |= ((uint32_t)(int)rintf(c[i]) & 0xffu) << (8 * (i & 3));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        int p = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i], c[4 * i + 1], 0, false);
-        b[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i + 2], c[4 * i + 3], p, true);
+    for (int k = 0; k < K; ++k) {
+      if (a.in_group || k == 0) {
+        const float top = a.in_group ? most[k] : all;
+        float scale = top * rs / M;
+        if (scale < 0x1p-126f) scale = 0.f;
+        by = factor_of(top, scale, M);
+        const int lanes = a.in_group ? a.in_group : a.tpr;
+        if (mine && n[k] > 0 && in_row % lanes == 0)
+          a.scales[r * a.ss + (a.in_group ? (in_row + k * a.tpr) / lanes : 0)] = scale;
       }
-    }
-    uint8_t* out = a.q + r * a.sq + col;
-    if (n >= 8) {
-      typedef uint32_t W2 __attribute__((ext_vector_type(2)));
-      typedef W2 Any __attribute__((aligned(1)));
-      store_global<Any>(out, 0, W2{b[0], b[1]});
-    } else {
+      if (!mine || n[k] <= 0) continue;
+      float c[8];
 #pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (i < n) out[i] = (uint8_t)(b[i >> 2] >> (8 * (i & 3)));
+      for (int i = 0; i < 8; ++i) {
+        const float p = v[k][i] * w[k][i], rest = fmaf(v[k][i], w[k][i], -p);
+        const float q = fmaf(p, by.hi, fmaf(p, by.lo, rest * by.hi));
+        c[i] = by.on ? __builtin_amdgcn_fmed3f(q, -M, M) : 0.f;
+      }
+      uint32_t b[2] = {0, 0};
+      if (CODE == SGB_CODE_INT8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          b[i >> 2] |= ((uint32_t)(int)rintf(c[i]) & 0xffu) << (8 * (i & 3));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int p = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i], c[4 * i + 1], 0, false);
+          b[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * i + 2], c[4 * i + 3], p, true);
+        }
+      }
+      uint8_t* out = a.q + r * a.sq + col[k];
+      if (n[k] >= 8) {
+        typedef uint32_t W2 __attribute__((ext_vector_type(2)));
+        typedef W2 Any __attribute__((aligned(1)));
+        store_global<Any>(out, 0, W2{b[0], b[1]});
+      } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (i < n[k]) out[i] = (uint8_t)(b[i >> 2] >> (8 * (i & 3)));
+      }
     }
   }
 }
 
-template <typename T, typename U, int CODE>
-void launch(const Args& a, unsigned grid, int threads, hipStream_t s) {
+template <typename T, typename U, int CODE, bool RES>
+void launch_as(const Args& a, unsigned grid, int threads, hipStream_t s) {
   const dim3 g(grid), b(threads);
   if (a.D < 8)
-    hipLaunchKernelGGL((k_quant<T, U, CODE, false, true>), g, b, 0, s, a);
-  else if (a.tpr > 64)
-    hipLaunchKernelGGL((k_quant<T, U, CODE, true, false>), g, b, 0, s, a);
+    hipLaunchKernelGGL((k_quant<T, U, CODE, false, 1, RES, true>), g, b, 0, s, a);
+  else if (a.D > a.tpr * 8)
+    hipLaunchKernelGGL((k_quant<T, U, CODE, true, 2, RES, false>), g, b, 0, s, a);
+  else if (a.tpr >= 64)
+    hipLaunchKernelGGL((k_quant<T, U, CODE, true, 1, RES, false>), g, b, 0, s, a);
   else
-    hipLaunchKernelGGL((k_quant<T, U, CODE, false, false>), g, b, 0, s, a);
+    hipLaunchKernelGGL((k_quant<T, U, CODE, false, 1, RES, false>), g, b, 0, s, a);
+}
+
+template <typename T, typename U, int CODE>
+void launch(const Args& a, unsigned grid, int threads, hipStream_t s) {
+  if (a.x)
+    launch_as<T, U, CODE, true>(a, grid, threads, s);
+  else
+    launch_as<T, U, CODE, false>(a, grid, threads, s);
 }
 
 template <typename T, typename U>
@@ -264,11 +317,12 @@ sgb_status sgb_quant_norm_forward(sgb_quant_norm p, const sgb_quant_norm_args* q
   a.eps = p->eps;
   a.inv_d = 1.f / (float)D;
   a.in_group = p->group < D ? p->group / 8 : 0;  // one group: the row's team may be narrower
+  // Two vectors a lane from 1024 columns on: half the waves to fold over.
   a.tpr = 8;
-  while (a.tpr * 8 < D) a.tpr *= 2;
+  while (a.tpr * (D > 1024 ? 16 : 8) < D) a.tpr *= 2;
   DeviceGuard guard(p->device);
   if (!guard.ok) return SGB_ERR_HIP;
-  const int threads = a.tpr > 256 ? a.tpr : 256;
+  const int threads = std::max(a.tpr, 256);
   const int64_t rows_a_block = threads / a.tpr;
   const int64_t most = (int64_t)p->cus * (2048 / threads);
   const unsigned grid = (unsigned)std::min(div_up(R, rows_a_block), most);
