@@ -38,15 +38,13 @@ constexpr int64_t kMaxV = 1 << 23;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kUp = 32768.f;   // 2^15: see above; fp16 gradients are scaled by it too
 
-typedef float Acc __attribute__((ext_vector_type(16)));
 typedef float F4 __attribute__((ext_vector_type(4)));
-typedef F4 F4Any __attribute__((aligned(4)));
 
-__device__ __forceinline__ Acc mfma(Vec<bf16_t>::type a, Vec<bf16_t>::type b, Acc c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ F4 mfma(Vec<bf16_t>::type a, Vec<bf16_t>::type b, F4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ Acc mfma(Vec<f16_t>::type a, Vec<f16_t>::type b, Acc c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ F4 mfma(Vec<f16_t>::type a, Vec<f16_t>::type b, F4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -176,21 +174,21 @@ __device__ __forceinline__ F4 load4(const void* row, int64_t at, int64_t n) {
   return v;
 }
 
-// A wave's results on their way out, through LDS of its own: 32 of B's rows by
-// FRAGS times 32 of A's, put in as the matrix instruction leaves them (four
+// A wave's results on their way out, through LDS of its own: 16 of B's rows by
+// FRAGS times 16 of A's, put in as the matrix instruction leaves them (four
 // neighbours of a row a lane) and got as 16 bytes of whole rows, so that a store
 // fills lines.  Exponentials of 8192 x 131072 logits of 4096, bf16: 7.5 ms with
 // stores of what a lane holds, 7.3 so; of 1021 x 50021 of 1001, fp16: 175 and 163 us.
 template <typename O, int FRAGS>
-struct Rows32 {
-  static constexpr int kFrags = FRAGS, kRow = FRAGS * 32 * (int)sizeof(O), kPitch = kRow + 16;
-  static constexpr int kBytes = 32 * kPitch, kLanes = kRow / 16, kTurns = kLanes / 2;
+struct Rows16 {
+  static constexpr int kFrags = FRAGS, kRow = FRAGS * 16 * (int)sizeof(O), kPitch = kRow + 16;
+  static constexpr int kBytes = 16 * kPitch, kLanes = kRow / 16, kTurns = kLanes / 4;
   typedef O Words __attribute__((ext_vector_type(16 / sizeof(O))));
-  static __device__ __forceinline__ void put(char* lds, int lane, int i, int k, F4 v) {
+  static __device__ __forceinline__ void put(char* lds, int lane, int i, F4 v) {
     typedef O O4 __attribute__((ext_vector_type(4)));
     const O4 o = {(O)v[0], (O)v[1], (O)v[2], (O)v[3]};
-    *reinterpret_cast<O4*>(lds + (lane & 31) * kPitch +
-                           (32 * i + 2 * k + 4 * (lane >> 5)) * (int)sizeof(O)) = o;
+    *reinterpret_cast<O4*>(lds + (lane & 15) * kPitch +
+                           (16 * i + 4 * (lane >> 4)) * (int)sizeof(O)) = o;
   }
   static __device__ __forceinline__ int row(int lane, int turn) {
     return turn * (64 / kLanes) + lane / kLanes;
@@ -203,17 +201,19 @@ struct Rows32 {
   }
 };
 
-// f of both halves of a wave.
+// f over the lanes 16 apart.
 template <typename F>
-__device__ __forceinline__ float halves(float x, F f) {
-  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return f(__uint_as_float(s[0]), __uint_as_float(s[1]));
+__device__ __forceinline__ float quarters(float x, F f) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 template <typename E, int TERMS, int EPI, typename C>
 __device__ __forceinline__ void product_tile(const Product& p, int block) {
   constexpr int TM = C::TM, TN = C::TN, WM = C::WM, WN = C::WN;
-  constexpr int WAVES = kThreadsOf<C> / 64, FM = WM / 32, FN = WN / 32;
+  constexpr int WAVES = kThreadsOf<C> / 64, FM = WM / 16, FN = WN / 16;
   constexpr int kBytes = (TM + TN) * kRowBytes;
   // (variables of their own: a read of one does not wait for loads to the other)
   __shared__ __attribute__((aligned(1024))) char buf0[C::kSteps * kBytes], buf1[C::kSteps * kBytes];
@@ -263,36 +263,34 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
     __builtin_amdgcn_sched_barrier(0);  // (the compiler would put them off)
   };
 
-  Acc acc[FM][FN];
+  F4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
+    for (int j = 0; j < FN; ++j) acc[i][j] = F4{0.f, 0.f, 0.f, 0.f};
 
-  // A step is four of 16, each with its fragments read while the step before
+  // A step is two of 32, each with its fragments read while the one before
   // multiplies.  A turn's last products come after the barrier that frees its
   // buffer, and cover the next turn's first reads.
   typedef typename Vec<E>::type V8;
   V8 fa[2][FM], fb[2][FN];
-  const int key = (lane >> 1) & 7, row = (lane & 31) * kRowBytes;
+  const int key = (lane >> 1) & 7, row = (lane & 15) * kRowBytes;
   const auto read = [&](const char* buf, int kk) {
-    const int at = row + ((kk * 2 + (lane >> 5)) ^ key) * 16;
+    const int at = row + ((kk * 4 + (lane >> 4)) ^ key) * 16;
     const uint32_t ra = wm * kRowBytes + at, rb = (TM + wn) * kRowBytes + at;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      fa[kk & 1][i] = *reinterpret_cast<const V8*>(buf + (ra + i * 32 * kRowBytes));
-#pragma unroll
     for (int j = 0; j < FN; ++j)
-      fb[kk & 1][j] = *reinterpret_cast<const V8*>(buf + (rb + j * 32 * kRowBytes));
+      fb[kk][j] = *reinterpret_cast<const V8*>(buf + (rb + j * 16 * kRowBytes));
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      fa[kk][i] = *reinterpret_cast<const V8*>(buf + (ra + i * 16 * kRowBytes));
   };
   const auto multiply = [&](int kk) {
     constexpr int kEach = FM * FN / (FM + FN);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = mfma(fa[kk & 1][i], fb[kk & 1][j], acc[i][j]);
+      for (int j = 0; j < FN; ++j) acc[i][j] = mfma(fa[kk][i], fb[kk][j], acc[i][j]);
 #pragma unroll
     for (int i = 0; i < FM + FN; ++i) {  // one read, then one or more products
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -301,20 +299,17 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
     __builtin_amdgcn_sched_group_barrier(0x008, FM * FN - kEach * (FM + FN), 0);
   };
   // a turn's steps but the last of their products
-  const auto three = [&](const char* buf) {
-#pragma unroll
-    for (int kk = 0; kk < 3; ++kk) {
-      read(buf, kk + 1);
-      multiply(kk);
-    }
+  const auto most = [&](const char* buf) {
+    read(buf, 1);
+    multiply(0);
   };
   const auto turn = [&](const char* buf) {
 #pragma unroll
     for (int s = 0; s < C::kSteps; ++s) {
-      three(buf + s * kBytes);
+      most(buf + s * kBytes);
       if (s + 1 == C::kSteps) break;
       read(buf + (s + 1) * kBytes, 0);
-      multiply(3);
+      multiply(1);
     }
   };
 
@@ -328,58 +323,53 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
     all_loaded();
     stage(buf0);
     read(buf1, 0);
-    multiply(3);
+    multiply(1);
     turn(buf1);
     all_loaded();
     stage(buf1);
     read(buf0, 0);
-    multiply(3);
+    multiply(1);
   }
   if (left > 1) {
     turn(buf0);
     all_loaded();
     read(buf1, 0);
-    multiply(3);
+    multiply(1);
   }
   const char* buf = left > 1 ? buf1 : buf0;
-  three(buf);
+  most(buf);
   for (int s = (turns - 1) * C::kSteps + 1; s < steps; ++s) {  // (none where a turn is one step)
     buf += kBytes;
     read(buf, 0);
-    multiply(3);
-    three(buf);
+    multiply(1);
+    most(buf);
   }
-  multiply(3);
+  multiply(1);
   all_loaded();  // LDS is free: no load to it is under way any more
 
-  // acc[i][j][k]: C's row (of A) m0 + wm + 32 i + 8 (k / 4) + 4 (lane / 32) +
-  // k % 4, its column (of B) n0 + wn + 32 j + lane % 32
-  const int64_t mw = m0 + wm + 4 * (lane >> 5);
-  char* own = (wave < WAVES / 2 ? buf0 : buf1) + wave % (WAVES / 2) * Rows32<float, 2>::kBytes;
+  // acc[i][j][k]: C's row (of A) m0 + wm + 16 i + 4 (lane / 16) + k, its column
+  // (of B) n0 + wn + 16 j + lane % 16
+  const int64_t mw = m0 + wm + 4 * (lane >> 4);
+  char* own = (wave < WAVES / 2 ? buf0 : buf1) + wave % (WAVES / 2) * Rows16<float, 4>::kBytes;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    __builtin_amdgcn_sched_barrier(0);  // (both at once would spill)
-    const int64_t nw = n0 + wn + 32 * j, n = nw + (lane & 31);
+    __builtin_amdgcn_sched_barrier(0);  // (all at once would spill)
+    const int64_t nw = n0 + wn + 16 * j, n = nw + (lane & 15);
     const bool there = n < p.N;
     if constexpr (EPI == kGrads) {
       float by = 1.f;
       if (!p.sums)
         by = p.scale * (!p.by_row ? value_or(p.most, 0, 1.f) : there ? factor_of(p.rows, n) : 0.f);
-      typedef Rows32<float, (FM > 1 ? 2 : 1)> L;
+      typedef Rows16<float, (FM < 4 ? FM : 4)> L;
 #pragma unroll
       for (int i0 = 0; i0 < FM; i0 += L::kFrags) {
 #pragma unroll
-        for (int i = 0; i < L::kFrags; ++i)
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const Acc& c = acc[i0 + i][j];
-            L::put(own, lane, i, k, F4{c[k], c[k + 1], c[k + 2], c[k + 3]});
-          }
+        for (int i = 0; i < L::kFrags; ++i) L::put(own, lane, i, acc[i0 + i][j]);
 #pragma unroll
         for (int u = 0; u < L::kTurns; ++u) {
           const int r = L::row(lane, u);
           const float scale = __shfl(by, r);
-          const int64_t at = nw + r, m = m0 + wm + 32 * i0 + L::col(lane), n4 = p.M - m;
+          const int64_t at = nw + r, m = m0 + wm + 16 * i0 + L::col(lane), n4 = p.M - m;
           F4 v = L::get(own, lane, u);
           if (at >= p.N || n4 <= 0) continue;
           if (p.sums) {
@@ -415,55 +405,52 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
 #pragma unroll
           for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (mw + 32 * i + 8 * (k >> 2) + (k & 3) >= p.M) acc[i][j][k] = -INFINITY;
+            for (int k = 0; k < 4; ++k)
+              if (mw + 16 * i + k >= p.M) acc[i][j][k] = -INFINITY;
         }
         const int64_t label = there ? p.rows.labels[n] - (p.v0 + m0 + wm) : -1;
         if (label >= 0 && label < WM && label + m0 + wm < p.M) {
 #pragma unroll
           for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (label == 32 * i + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3))
-                p.said[n] = acc[i][j][k];
+            for (int k = 0; k < 4; ++k)
+              if (label == 16 * i + 4 * (lane >> 4) + k) p.said[n] = acc[i][j][k];
         }
         top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-          for (int k = 0; k < 16; ++k) top = fmaxf(top, acc[i][j][k]);
-        top = halves(top, [](float x, float y) { return fmaxf(x, y); });
+          for (int k = 0; k < 4; ++k) top = fmaxf(top, acc[i][j][k]);
+        top = quarters(top, [](float x, float y) { return fmaxf(x, y); });
         if (top == -INFINITY) top = 0.f;  // nothing but -inf: the sum is 0
       }
-      typedef Rows32<X, (FM < 8 / (int)sizeof(X) ? FM : 8 / (int)sizeof(X))> L;
+      typedef Rows16<X, (FM < 16 / (int)sizeof(X) ? FM : 16 / (int)sizeof(X))> L;
 #pragma unroll
       for (int i0 = 0; i0 < FM; i0 += L::kFrags) {
 #pragma unroll
-        for (int i = 0; i < L::kFrags; ++i)
+        for (int i = 0; i < L::kFrags; ++i) {
+          F4 v;
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            F4 v;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              v[u] = exp2_((acc[i0 + i][j][k + u] - top) * kLog2e);
-              sum += v[u];
-            }
-            if (EPI != kSums) L::put(own, lane, i, k, v * (sizeof(X) == 2 ? kUp : 1.f));
+          for (int k = 0; k < 4; ++k) {
+            v[k] = exp2_((acc[i0 + i][j][k] - top) * kLog2e);
+            sum += v[k];
           }
+          if (EPI != kSums) L::put(own, lane, i, v * (sizeof(X) == 2 ? kUp : 1.f));
+        }
         if constexpr (EPI != kSums) {
 #pragma unroll
           for (int u = 0; u < L::kTurns; ++u) {
             const int64_t at = nw + L::row(lane, u);
             const auto v = L::get(own, lane, u);
             if (at >= p.N) continue;
-            X* out = static_cast<X*>(p.exps) + at * p.ld_exps + (p.v0 + m0 + wm + 32 * i0 + L::col(lane));
+            X* out = static_cast<X*>(p.exps) + at * p.ld_exps + (p.v0 + m0 + wm + 16 * i0 + L::col(lane));
             *reinterpret_cast<typename L::Words*>(out) = v;
           }
         }
       }
       if constexpr (EPI != kProbs) {
-        sum = halves(sum, [](float x, float y) { return x + y; });
-        if (there && lane < 32)
+        sum = quarters(sum, [](float x, float y) { return x + y; });
+        if (there && lane < 16)
           p.stats[(p.v0 + m0 + wm) / WM * p.tokens + n] = make_float2(top, sum);
       }
     }
