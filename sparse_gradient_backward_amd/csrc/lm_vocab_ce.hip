@@ -58,6 +58,9 @@ constexpr int kRowBytes = kStep * 2;
 struct Big {  // one workgroup a compute unit, for products that give each one
   static constexpr int TM = 256, TN = 256, WM = 128, WN = 64, kSteps = 1;
 };
+struct BigOther : Big {  // fewer fragments of the operand that is read transposed
+  static constexpr int WM = 64, WN = 128;
+};
 struct Medium {  // two, one at its start or end while the other multiplies
   static constexpr int TM = 128, TN = 128, WM = 64, WN = 64, kSteps = 1;
 };
@@ -67,7 +70,11 @@ struct Tiny {  // for the time that loads take, not for how many there are
 template <typename C>
 constexpr int kThreadsOf = C::TM / C::WM * (C::TN / C::WN) * 64;
 
+template <typename C>
+constexpr int kBufBytes = C::kSteps * (C::TM + C::TN) * kRowBytes;
+
 enum Epilogue { kSums, kExps, kProbs, kGrads };
+enum ByRow { kPlain, kKept, kScaled };
 
 // What says how much a row counts.
 struct Rows {
@@ -85,7 +92,8 @@ struct Product {
   const char *a, *b;
   int64_t lda, ldb;          // bytes from row to row; of 16
   int64_t plane_a, plane_b;  // bytes from one bf16 part of fp32 operands to the next
-  int64_t M, N;              // rows of a, b
+  int64_t M, N;              // rows of a, b; of an operand held the other way, columns,
+  int64_t cols_a, cols_b;    // of which so many can be read
   int steps, split;          // of the summed dimension, over 1..steps workgroups
   int tm, tn;
   Rows rows;
@@ -105,13 +113,28 @@ struct Product {
   const float* add_from;     // [N][M] or null
   const float* most;         // (null: 1) times scale: what the sums are multiplied by
   float scale;
-  bool by_row;               // d_hidden: times the row's factor too, add_from with them
+  int by_row;                // d_hidden, add_from with it: kScaled, or only kept (0 for
+                             // a row that does not count)
 };
 
 // Which bf16 parts (0: the highest) the products of fp32 operands are of, the
 // smallest first; those left out are below 2^-25 of the whole.
 constexpr uint32_t kPartsA = 0u << 0 | 2u << 2 | 1u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
 constexpr uint32_t kPartsB = 2u << 0 | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
+
+// 1 KB a wave and load to consecutive addresses of LDS, from `base`, the same for
+// all lanes, and a lane's offset (a buffer's load: no addresses of 64 bits).
+template <int J>
+__device__ __forceinline__ void load_to_lds(const char* base, const uint32_t (&off)[J], char* lds) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const __amdgpu_buffer_rsrc_t from =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, -1, 0x00027000);
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        from, (__attribute__((address_space(3))) void*)(lds + j * 1024), 16, off[j], 0, 0, 0);
+#endif
+}
 
 // The workgroup's loads of R rows of 64 elements, straight to LDS, 16 bytes a
 // lane.  A row is 128 bytes of LDS; its 16-byte parts are stored in an order
@@ -132,13 +155,34 @@ struct Stage {
     }
   }
   __device__ __forceinline__ void load(const char* base, char* lds, int wave) const {
-#ifdef __HIP_DEVICE_COMPILE__
+    load_to_lds(base, off, lds + wave * (J * 1024));
+  }
+};
+
+// The same of an operand held the other way, the summed dimension from row to
+// row: 64 rows of R elements.  A matrix instruction's operand is read from it
+// transposed, 16 lanes at a time from four rows of 32 bytes; the rows' pieces of
+// 32 bytes are stored in an order that puts those of eight such rows into
+// different banks.
+template <int R>
+__device__ __forceinline__ int order_of(int row) {  // for rows of 128 bytes, two to a round of banks
+  return R > 64 ? (row & 3) | (row >> 3 & 1) << 2 : (row >> 1 & 1) | (row >> 3 & 1) << 1;
+}
+template <int R, int WAVES>
+struct StageOther {
+  static constexpr int J = R / (8 * WAVES);
+  uint32_t off[J];
+  __device__ __forceinline__ void init(int wave, int lane, int64_t left, int64_t ld) {
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(base + off[j]),
-          (__attribute__((address_space(3))) void*)(lds + (wave * J + j) * 1024), 16, 0, 0);
-#endif
+    for (int j = 0; j < J; ++j) {
+      const int at = (wave * J + j) * 64 + lane;  // 16 bytes each
+      const int row = at / (R / 8), part = at % (R / 8) ^ order_of<R>(row) << 1;
+      // columns past the last are copies of others
+      off[j] = (uint32_t)row * (uint32_t)ld + (uint32_t)min((int64_t)part, left / 8 - 1) * 16;
+    }
+  }
+  __device__ __forceinline__ void load(const char* base, char* lds, int wave) const {
+    load_to_lds(base, off, lds + wave * (J * 1024));
   }
 };
 
@@ -210,13 +254,12 @@ __device__ __forceinline__ float quarters(float x, F f) {
   return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-template <typename E, int TERMS, int EPI, typename C>
-__device__ __forceinline__ void product_tile(const Product& p, int block) {
+// AO, BO: the operand is held the other way.
+template <typename E, int TERMS, int EPI, typename C, bool AO, bool BO>
+__device__ __forceinline__ void product_tile(const Product& p, int block, char* buf0, char* buf1) {
   constexpr int TM = C::TM, TN = C::TN, WM = C::WM, WN = C::WN;
   constexpr int WAVES = kThreadsOf<C> / 64, FM = WM / 16, FN = WN / 16;
   constexpr int kBytes = (TM + TN) * kRowBytes;
-  // (variables of their own: a read of one does not wait for loads to the other)
-  __shared__ __attribute__((aligned(1024))) char buf0[C::kSteps * kBytes], buf1[C::kSteps * kBytes];
 
   // Workgroups go round the eight dies; each die gets a run of tiles of its
   // own, eight tiles of A by some of B at a time, whose operands its L2 shares.
@@ -234,11 +277,11 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % (TM / WM) * WM, wn = wave / (TM / WM) * WN;
 
-  Stage<TM, WAVES> sa;
-  Stage<TN, WAVES> sb;
-  sa.init(wave, lane, p.M - m0, p.lda);
-  sb.init(wave, lane, p.N - n0, p.ldb);
-  const char *a = p.a + m0 * p.lda, *b = p.b + n0 * p.ldb;
+  typename std::conditional<AO, StageOther<TM, WAVES>, Stage<TM, WAVES>>::type sa;
+  typename std::conditional<BO, StageOther<TN, WAVES>, Stage<TN, WAVES>>::type sb;
+  sa.init(wave, lane, (AO ? p.cols_a : p.M) - m0, p.lda);
+  sb.init(wave, lane, (BO ? p.cols_b : p.N) - n0, p.ldb);
+  const char *a = p.a + m0 * (AO ? 2 : p.lda), *b = p.b + n0 * (BO ? 2 : p.ldb);
   const int from = (int)((int64_t)p.steps * part / p.split);
   const int to = (int)((int64_t)p.steps * (part + 1) / p.split);
   const int steps = (to - from) * TERMS, turns = (steps + C::kSteps - 1) / C::kSteps;
@@ -248,8 +291,8 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
   const auto stage = [&](char* buf) {
 #pragma unroll
     for (int s = 0; s < C::kSteps; ++s) {
-      const int64_t at = (int64_t)step * kRowBytes;
-      const char *pa = a + at, *pb = b + at;
+      const char* pa = a + step * (AO ? kStep * p.lda : kRowBytes);
+      const char* pb = b + step * (BO ? kStep * p.ldb : kRowBytes);
       if (TERMS > 1) {
         pa += (kPartsA >> (2 * term) & 3) * p.plane_a;
         pb += (kPartsB >> (2 * term) & 3) * p.plane_b;
@@ -275,28 +318,60 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
   typedef typename Vec<E>::type V8;
   V8 fa[2][FM], fb[2][FN];
   const int key = (lane >> 1) & 7, row = (lane & 15) * kRowBytes;
+  // held the other way: 4 of a lane's 8 elements from 4 rows by 16 columns
+  const auto other = [&](const char* at, int wide) -> V8 {
+    typedef short H __attribute__((ext_vector_type(4)));
+    struct {
+      H lo, hi;
+    } v{};
+#ifdef __HIP_DEVICE_COMPILE__
+    v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) H*)at);
+    v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) H*)(at + 4 * wide));
+#endif
+    return __builtin_bit_cast(V8, v);
+  };
+  const int r4 = 8 * (lane >> 4) + (lane >> 2 & 3);  // this lane's first row of a step of 32
+  const uint32_t at_a = r4 * TM * 2 + (lane & 3) * 8 + (wm / 16 ^ order_of<TM>(r4)) * 32;
+  const uint32_t at_b = r4 * TN * 2 + (lane & 3) * 8 + (wn / 16 ^ order_of<TN>(r4)) * 32;
   const auto read = [&](const char* buf, int kk) {
     const int at = row + ((kk * 4 + (lane >> 4)) ^ key) * 16;
-    const uint32_t ra = wm * kRowBytes + at, rb = (TM + wn) * kRowBytes + at;
+    // (one address a fragment, made when it is needed: kept, they would spill)
+    uint32_t oa = at_a, ob = at_b;
+    if (AO) asm volatile("" : "+v"(oa));
+    if (BO) asm volatile("" : "+v"(ob));
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      fb[kk][j] = *reinterpret_cast<const V8*>(buf + (rb + j * 16 * kRowBytes));
+    for (int j = 0; j < FN; ++j) {
+      if constexpr (BO)
+        fb[kk][j] = other(buf + (TM * kRowBytes + kk * 32 * TN * 2 + (ob ^ j * 32)), TN * 2);
+      else
+        fb[kk][j] = *reinterpret_cast<const V8*>(buf + (uint32_t)((TM + wn) * kRowBytes + at + j * 16 * kRowBytes));
+    }
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      fa[kk][i] = *reinterpret_cast<const V8*>(buf + (ra + i * 16 * kRowBytes));
+    for (int i = 0; i < FM; ++i) {
+      if constexpr (AO)
+        fa[kk][i] = other(buf + (kk * 32 * TM * 2 + (oa ^ i * 32)), TM * 2);
+      else
+        fa[kk][i] = *reinterpret_cast<const V8*>(buf + (uint32_t)(wm * kRowBytes + at + i * 16 * kRowBytes));
+    }
   };
   const auto multiply = [&](int kk) {
-    constexpr int kEach = FM * FN / (FM + FN);
+    // Products and reads in turn.  The first products come before any read: they
+    // free their operands' registers for it.
+    constexpr int kReads = FM * (1 + AO) + FN * (1 + BO), kAll = FM * FN;
+    constexpr int kLead = kAll > kReads ? kAll - kReads < 8 ? kAll - kReads : 8 : 0;
+    constexpr int kEach = kAll - kLead < kReads ? 1 : (kAll - kLead) / kReads;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = mfma(fa[kk][i], fb[kk][j], acc[i][j]);
+    if (kLead) __builtin_amdgcn_sched_group_barrier(0x008, kLead, 0);
 #pragma unroll
-    for (int i = 0; i < FM + FN; ++i) {  // one read, then one or more products
+    for (int i = 0; i < kReads && i < kAll; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, FM * FN - kEach * (FM + FN), 0);
+    if (kAll > kLead + kEach * kReads)
+      __builtin_amdgcn_sched_group_barrier(0x008, kAll - kLead - kEach * kReads, 0);
   };
   // a turn's steps but the last of their products
   const auto most = [&](const char* buf) {
@@ -359,7 +434,10 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
     if constexpr (EPI == kGrads) {
       float by = 1.f;
       if (!p.sums)
-        by = p.scale * (!p.by_row ? value_or(p.most, 0, 1.f) : there ? factor_of(p.rows, n) : 0.f);
+        by = p.scale * (p.by_row == kPlain ? value_or(p.most, 0, 1.f)
+                        : !there           ? 0.f
+                        : p.by_row == kKept ? (factor_of(p.rows, n) != 0.f ? 1.f : 0.f)
+                                            : factor_of(p.rows, n));
       typedef Rows16<float, (FM < 4 ? FM : 4)> L;
 #pragma unroll
       for (int i0 = 0; i0 < FM; i0 += L::kFrags) {
@@ -380,7 +458,7 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
           }
           F4 more = {0.f, 0.f, 0.f, 0.f};
           if (p.add_from) more = load4<float>(p.add_from + at * p.M, m, n4);
-          if (p.by_row)
+          if (p.by_row != kPlain)
             v = scale == 0.f ? F4{0.f, 0.f, 0.f, 0.f} : (v + more) * scale;
           else
             v = v * scale + more;
@@ -457,15 +535,23 @@ __device__ __forceinline__ void product_tile(const Product& p, int block) {
   }
 }
 
-// `q`: a second product of the same kind, in workgroups from `first` on.
-template <typename E, int TERMS, int EPI, typename C>
-__global__ __launch_bounds__(kThreadsOf<C>, 2) void k_product(Product p, Product q, int first) {
-  int block = (int)blockIdx.x;
-  if (block >= first) {
-    p = q;
-    block -= first;
-  }
-  product_tile<E, TERMS, EPI, C>(p, block);
+// (buf0, buf1: variables of their own, so that a read of one does not wait for
+// loads to the other)
+template <typename E, int TERMS, int EPI, typename C, bool AO, bool BO>
+__global__ __launch_bounds__(kThreadsOf<C>, 2) void k_product(Product p) {
+  __shared__ __attribute__((aligned(1024))) char buf0[kBufBytes<C>], buf1[kBufBytes<C>];
+  product_tile<E, TERMS, EPI, C, AO, BO>(p, (int)blockIdx.x, buf0, buf1);
+}
+
+// d_hidden in the first workgroups, d_weight in the others.
+template <typename E, int TERMS, typename C>
+__global__ __launch_bounds__(kThreadsOf<C>, 2) void k_products(Product h, Product w, int first) {
+  __shared__ __attribute__((aligned(1024))) char buf0[kBufBytes<C>], buf1[kBufBytes<C>];
+  const int block = (int)blockIdx.x;
+  if (block < first)
+    product_tile<E, TERMS, kGrads, C, true, false>(h, block, buf0, buf1);
+  else
+    product_tile<E, TERMS, kGrads, C, false, true>(w, block - first, buf0, buf1);
 }
 
 // ---------------------------------------------------------------- copies
@@ -493,8 +579,6 @@ struct Parts<float> {
   }
 };
 
-constexpr int kTile = 64;
-
 template <typename T, typename V>
 __device__ __forceinline__ void store_parts(const V (&v)[8], typename Parts<T>::E* to, int64_t plane) {
   typedef typename Parts<T>::E E;
@@ -512,9 +596,12 @@ __device__ __forceinline__ void store_parts(const V (&v)[8], typename Parts<T>::
     *reinterpret_cast<uint4*>(to + k * plane) = *reinterpret_cast<const uint4*>(out[k]);
 }
 
-// An operand's rows [rows][D] as the product reads them: [rows][pitch] with zeros
-// past D, transposed to [D][pitch_t] with zeros past the last row (and, with
-// `only`, in rows that do not count: what they hold may be no number), or both.
+constexpr int kTile = 64;
+
+// An operand's rows [rows][D] as the products read them: [up(rows)][pitch] with
+// zeros past D and past the last row; transposed to [D][pitch_t] with zeros past
+// the last row and in rows that do not count (what they hold may be no number);
+// or both.
 template <typename T>
 struct Copy {
   typedef typename Parts<T>::E E;
@@ -523,7 +610,6 @@ struct Copy {
   int D;
   E *to, *to_t;  // or null
   int64_t pitch, plane, pitch_t, plane_t;
-  bool only;
   Rows count;
 };
 
@@ -545,12 +631,13 @@ __global__ __launch_bounds__(256) void k_copy(Copy<T> a, Copy<T> b, unsigned fir
     const int r = (t >> 3) + 32 * u, c = (t & 7) * 8;
     const bool there = r0 + r < a.rows;
     Raw8<T> raw = load8(a.src + (r0 + r) * a.stride + d0 + c, there ? min(8, a.D - d0 - c) : 0);
-    if (a.to && there) {
+    if (a.to) {
       T v[8];
       __builtin_memcpy(v, &raw, sizeof v);
       store_parts<T>(v, a.to + (r0 + r) * a.pitch + d0 + c, a.plane);
     }
-    const bool on = there && (!a.only || factor_of(a.count, r0 + r) != 0.f);
+    if (!a.to_t) continue;
+    const bool on = there && factor_of(a.count, r0 + r) != 0.f;
     uint32_t* row = reinterpret_cast<uint32_t*>(&tile[r][c]);
 #pragma unroll
     for (int i = 0; i < Vec<T>::kWords; ++i) row[i] = on ? raw.w[i] : 0u;
@@ -660,18 +747,17 @@ struct Grad {
   const float* lse;
   const float* most;  // null: 1
   int64_t v0, width;  // the piece
-  void *g, *gt;       // [tokens][pitch], [width][pitch_t], or null
-  int64_t pitch, plane, pitch_t, plane_t;
+  // over the row's factor, and with it (over the largest); or null
+  void *plain, *scaled;  // [up(tokens)][pitch]
+  int64_t pitch, plane;
 };
 
-// The gradient of a piece's logits from their exponentials: as it is (over the
-// row's factor) and transposed (with it), in the operands' type, zeros past the
-// vocabulary and past the last token.
+// The gradient of a piece's logits from their exponentials, in the operands'
+// type, zeros past the vocabulary and past the last token.
 template <typename T, typename X, bool SUM>
 __global__ __launch_bounds__(256) void k_grad(Grad q) {
   typedef typename Parts<T>::E E;
   constexpr float kBy = __is_same(T, f16_t) ? kUp : 1.f;  // fp16 has no room below 2^-24
-  __shared__ float tile[kTile][kTile + 1];
   __shared__ float2 part[SUM ? kShares : 1][SUM ? kTile : 1];
   const unsigned across = (unsigned)(q.pitch / kTile);
   const int64_t r0 = (int64_t)(blockIdx.x / across) * kTile;
@@ -739,27 +825,21 @@ __global__ __launch_bounds__(256) void k_grad(Grad q) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       v[i] = on && i < n ? (e[i] * k - (label[u] == i ? 1.f : 0.f)) * kBy : 0.f;
-    if (q.g && there) store_parts<T>(v, static_cast<E*>(q.g) + (r0 + lr) * q.pitch + c0 + c, q.plane);
+    const int64_t to = (r0 + lr) * q.pitch + c0 + c;
+    if (q.plain) store_parts<T>(v, static_cast<E*>(q.plain) + to, q.plane);
+    if (q.scaled) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tile[lr][c + i] = v[i] * share;
-  }
-  if (!q.gt) return;
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int lv = (t >> 3) + 32 * u, c = (t & 7) * 8;
-    if (c0 + lv >= q.width) continue;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = tile[c + i][lv];
-    store_parts<T>(v, static_cast<E*>(q.gt) + (c0 + lv) * q.pitch_t + r0 + c, q.plane_t);
+      for (int i = 0; i < 8; ++i) v[i] *= share;
+      store_parts<T>(v, static_cast<E*>(q.scaled) + to, q.plane);
+    }
   }
 }
 
 // d_hidden: the parts' sums in their order, the row's factor, one rounding.
 template <typename T>
 __global__ __launch_bounds__(256) void k_join(const float* sums, int split, int64_t rows, int D,
-                                              Rows count, float scale, T* out, int64_t stride) {
+                                              Rows count, bool scaled, float scale, T* out,
+                                              int64_t stride) {
   const int64_t groups = (D + 7) / 8, all = rows * groups;
   for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < all; g += (int64_t)gridDim.x * 256) {
     const int64_t r = g / groups;
@@ -775,7 +855,7 @@ __global__ __launch_bounds__(256) void k_join(const float* sums, int split, int6
         for (int i = 0; i < 8; ++i) v[i] += x[i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= f * scale;
+      for (int i = 0; i < 8; ++i) v[i] *= scaled ? f * scale : scale;
     }
     store8(out + r * stride + c, v, n);
   }
@@ -858,7 +938,7 @@ struct Layout {
   int64_t chunk, pad;  // rows a chunk, rounded up for the summed dimension
   int64_t piece;       // of the vocabulary
   int64_t pitch_d, ld_exps;
-  size_t lse, said, most, stats, x, w, wt, exps, g, gt, xt, sums, dw, bytes;
+  size_t lse, said, most, stats, x, xt, w, exps, plain, scaled, sums, dw, bytes;
 };
 
 Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
@@ -886,16 +966,15 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   l.said = take(4 * rows);
   l.most = take(4);
   l.stats = take(l.ld_exps / Tiny::WM * 8 * l.chunk);
-  l.x = take(l.chunk * l.pitch_d * part);
+  l.x = take(l.pad * l.pitch_d * part);
   // a piece's weight rows
   l.w = take(std::min(l.ld_exps, std::max<int64_t>(256, room / l.pitch_d)) * l.pitch_d * part);
   if (gradient) {
-    l.wt = take(std::min(l.ld_exps, std::max<int64_t>(256, room / l.pitch_d)) * D * part);
+    l.xt = take(D * l.pad * part);
     l.exps = take(l.chunk * l.ld_exps * exp_size);
     const int64_t grads = std::min(l.ld_exps * l.pad, std::max(room, 256 * l.pad)) * part;
-    l.g = take(grads);
-    l.gt = take(grads);
-    l.xt = take(D * l.pad * part);
+    l.scaled = take(grads);
+    if (dtype == SGB_F16) l.plain = take(grads);
     // a split's sums for any fewer rows too: at most 2 cus tiles
     const int64_t shared = 2ll * p->cus * Big::TM * Big::TN / D + 1;
     l.sums = take(std::max(l.chunk, std::min(kMaxSplit * l.chunk, shared)) * D * 4);
@@ -905,26 +984,24 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   return l;
 }
 
-template <typename E, int TERMS, int EPI, typename C>
-void launch(Product a, Product* b, hipStream_t s) {
-  const auto blocks = [](Product& p) {
-    p.tm = (int)div_up(p.M, C::TM);
-    p.tn = (int)div_up(p.N, C::TN);
-    return (unsigned)(div_up((int64_t)p.tm * p.tn * p.split, 8) * 8);
-  };
-  const unsigned first = blocks(a), second = b ? blocks(*b) : 0;
-  hipLaunchKernelGGL((k_product<E, TERMS, EPI, C>), dim3(first + second), dim3(kThreadsOf<C>), 0, s,
-                     a, b ? *b : a, (int)first);
+template <typename C>
+unsigned grid_of(Product& p) {
+  p.tm = (int)div_up(p.M, C::TM);
+  p.tn = (int)div_up(p.N, C::TN);
+  return (unsigned)(div_up((int64_t)p.tm * p.tn * p.split, 8) * 8);
 }
 
-template <typename E, int TERMS, int EPI>
-void product(const Product& a, Product* b, Tiles tiles, hipStream_t s) {
+template <typename E, int TERMS, int EPI, bool AO = false, bool BO = false>
+void product(Product p, Tiles tiles, hipStream_t s) {
   if (tiles == kBig)
-    launch<E, TERMS, EPI, Big>(a, b, s);
+    hipLaunchKernelGGL((k_product<E, TERMS, EPI, typename std::conditional<AO, BigOther, Big>::type, AO, BO>),
+                       dim3(grid_of<Big>(p)), dim3(kThreadsOf<Big>), 0, s, p);
   else if (tiles == kMedium)
-    launch<E, TERMS, EPI, Medium>(a, b, s);
+    hipLaunchKernelGGL((k_product<E, TERMS, EPI, Medium, AO, BO>), dim3(grid_of<Medium>(p)),
+                       dim3(kThreadsOf<Medium>), 0, s, p);
   else
-    launch<E, TERMS, EPI, Tiny>(a, b, s);
+    hipLaunchKernelGGL((k_product<E, TERMS, EPI, Tiny, AO, BO>), dim3(grid_of<Tiny>(p)),
+                       dim3(kThreadsOf<Tiny>), 0, s, p);
 }
 
 unsigned blocks(int64_t threads, int cus) {
@@ -976,49 +1053,56 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
   };
   if (most) hipLaunchKernelGGL(k_most, dim3(1), dim3(1024), 0, s, rows_at(0), R, most);
 
-  // Rows as the product reads them: whole 128-byte lines, 16-byte aligned, a
+  // Rows as the products read them: whole 128-byte lines, 16-byte aligned, a
   // tile's within 32 bits.
   const auto fits = [&](const void* a, int64_t stride, int64_t rows) {
     return sizeof(T) == 2 && D % kStep == 0 && aligned(a, 16) &&
            (rows < 2 || (stride % 8 == 0 && stride < (1 << 22)));
   };
+  const bool weight_fits = fits(weight, q->weight_stride, V);
   Copies<T> copies;
-  // Asks for a copy of rows (to) and of columns (to_t), where they are wanted.
-  const auto operands = [&](const T* src, int64_t stride, int64_t n, const Rows* only, E* to, E* to_t,
-                            Operand* rows, Operand* columns) {
+  const auto copy_of = [&](const T* src, int64_t stride, int64_t n) {
     Copy<T> c{src, stride, n, D};
     c.pitch = l.pitch_d;
-    c.plane = n * c.pitch;
+    c.plane = up(n, kStep) * c.pitch;
     c.pitch_t = up(n, kStep);
     c.plane_t = D * c.pitch_t;
-    if (only) {
-      c.only = true;
-      c.count = *only;
-    }
-    if (rows) {
-      if (fits(src, stride, n)) {
-        *rows = {reinterpret_cast<const char*>(src), stride * 2, 0};
-      } else {
-        c.to = to;
-        *rows = {reinterpret_cast<const char*>(to), c.pitch * 2, c.plane * 2};
-      }
-    }
-    if (columns) {
-      c.to_t = to_t;
-      *columns = {reinterpret_cast<const char*>(to_t), c.pitch_t * 2, c.plane_t * 2};
-    }
-    if (c.to || c.to_t) copies.c[copies.n++] = c;
+    return c;
+  };
+  const auto operand = [](const E* p, const Copy<T>& c) {
+    return Operand{reinterpret_cast<const char*>(p), c.pitch * 2, c.plane * 2};
+  };
+  // A piece of the weight; whole: its rows are read by whole steps, past the
+  // vocabulary where that is not one of steps.
+  const auto weight_rows = [&](int64_t v0, int64_t width, bool whole) {
+    const T* src = weight + v0 * q->weight_stride;
+    if (weight_fits && !(whole && v0 + width == V && V % kStep != 0))
+      return Operand{reinterpret_cast<const char*>(src), q->weight_stride * 2, 0};
+    Copy<T> c = copy_of(src, q->weight_stride, width);
+    c.to = elems(l.w);
+    copies.c[copies.n++] = c;
+    return operand(c.to, c);
   };
 
   // the logits by pieces only where the weight's rows have to be copied
-  const int64_t logits_piece = fits(weight, q->weight_stride, V) ? V : l.piece;
+  const int64_t logits_piece = weight_fits ? V : l.piece;
   const bool one_piece = l.piece >= V;
   for (int64_t r0 = 0; r0 < R; r0 += l.chunk) {
     const int64_t n = std::min(l.chunk, R - r0);
     const Rows rows = rows_at(r0);
-    Operand xo, xt, wo, wt;
-    operands(static_cast<const T*>(q->hidden) + r0 * q->hidden_stride, q->hidden_stride, n, &rows,
-             elems(l.x), elems(l.xt), &xo, grad && q->d_weight ? &xt : nullptr);
+    const T* x = static_cast<const T*>(q->hidden) + r0 * q->hidden_stride;
+    Copy<T> c = copy_of(x, q->hidden_stride, n);
+    Operand xo{reinterpret_cast<const char*>(x), q->hidden_stride * 2, 0}, xt{}, wo{};
+    if (!fits(x, q->hidden_stride, n)) {
+      c.to = elems(l.x);
+      xo = operand(c.to, c);
+    }
+    if (grad && q->d_weight) {
+      c.to_t = elems(l.xt);
+      c.count = rows;
+      xt = {reinterpret_cast<const char*>(c.to_t), c.pitch_t * 2, c.plane_t * 2};
+    }
+    if (c.to || c.to_t) copies.c[copies.n++] = c;
     Product a{};
     a.b = xo.p;
     a.ldb = xo.ld;
@@ -1036,8 +1120,8 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     const Tiles tiles = choose(std::min(logits_piece, V), n, a.steps, TERMS, p->cus, 1).tiles;
     for (int64_t v0 = 0; v0 < V; v0 += logits_piece) {
       const int64_t width = std::min(logits_piece, V - v0);
-      operands(weight + v0 * q->weight_stride, q->weight_stride, width, nullptr, elems(l.w),
-               elems(l.wt), &wo, grad && q->d_hidden && one_piece ? &wt : nullptr);
+      // (a single piece's copy serves d_hidden as well)
+      wo = weight_rows(v0, width, grad && q->d_hidden && one_piece);
       copies.launch(s);
       a.a = wo.p;
       a.lda = wo.ld;
@@ -1045,11 +1129,11 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       a.M = width;
       a.v0 = v0;
       if (way == kForward)
-        product<E, TERMS, kSums>(a, nullptr, tiles, s);
+        product<E, TERMS, kSums>(a, tiles, s);
       else if (way == kBoth)
-        product<E, TERMS, kExps>(a, nullptr, tiles, s);
+        product<E, TERMS, kExps>(a, tiles, s);
       else
-        product<E, TERMS, kProbs>(a, nullptr, tiles, s);
+        product<E, TERMS, kProbs>(a, tiles, s);
     }
     Loss loss{};
     loss.stats = a.stats;
@@ -1082,12 +1166,13 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       g.v0 = v0;
       g.width = width;
       g.pitch = up(width, kStep);
-      g.plane = n * g.pitch;
-      g.pitch_t = up(n, kStep);
-      g.plane_t = width * g.pitch_t;
-      g.g = q->d_hidden ? ws + l.g : nullptr;
-      g.gt = q->d_weight ? ws + l.gt : nullptr;
-      const dim3 grid((unsigned)(g.pitch / kTile * (g.pitch_t / kTile)));
+      g.plane = up(n, kStep) * g.pitch;
+      // Both products take the gradient with the row's factor; but fp16 could not
+      // hold that of a small one, and d_hidden takes it without.
+      constexpr bool kTwo = __is_same(T, f16_t);
+      if (q->d_weight || !kTwo) g.scaled = ws + l.scaled;
+      if (q->d_hidden && kTwo) g.plain = ws + l.plain;
+      const dim3 grid((unsigned)(g.pitch / kStep * (up(n, kStep) / kStep)));
       if (sum_later)
         hipLaunchKernelGGL((k_grad<T, X, true>), grid, dim3(256), 0, s, g);
       else
@@ -1095,23 +1180,23 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       Product h{}, w{};
       if (q->d_hidden) {
         if (!one_piece) {
-          operands(weight + v0 * q->weight_stride, q->weight_stride, width, nullptr, nullptr,
-                   elems(l.wt), nullptr, &wt);
+          wo = weight_rows(v0, width, true);
           copies.launch(s);
         }
-        h.a = wt.p;
-        h.lda = wt.ld;
-        h.plane_a = wt.plane;
-        h.b = static_cast<const char*>(g.g);
+        h.a = wo.p;
+        h.lda = wo.ld;
+        h.plane_a = wo.plane;
+        h.b = static_cast<const char*>(kTwo ? g.plain : g.scaled);
         h.ldb = g.pitch * 2;
         h.plane_b = g.plane * 2;
         h.M = D;
+        h.cols_a = l.pitch_d;
         h.N = n;
         h.steps = (int)(g.pitch / kStep);
         h.split = std::min(split, h.steps);
         if (split == 1 && v0 + width == V) {
           h.rows = rows;
-          h.by_row = true;
+          h.by_row = kTwo ? kScaled : kKept;
           h.scale = q->grad_scale / kBy;
           h.add_from = v0 > 0 ? floats(l.sums) : nullptr;
           h.out = static_cast<T*>(q->d_hidden) + r0 * q->d_hidden_stride;
@@ -1126,16 +1211,17 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       if (q->d_weight) {
         const bool first = r0 == 0, last = r0 + n == R;
         const bool direct = (first && last) || q->d_weight_dtype == SGB_F32;
-        tiles_w = choose(D, width, g.pitch_t / kStep, TERMS, p->cus, 1).tiles;
+        tiles_w = choose(D, width, up(n, kStep) / kStep, TERMS, p->cus, 1).tiles;
         w.a = xt.p;
         w.lda = xt.ld;
         w.plane_a = xt.plane;
-        w.b = static_cast<const char*>(g.gt);
-        w.ldb = g.pitch_t * 2;
-        w.plane_b = g.plane_t * 2;
+        w.b = static_cast<const char*>(g.scaled);
+        w.ldb = g.pitch * 2;
+        w.plane_b = g.plane * 2;
         w.M = D;
         w.N = width;
-        w.steps = (int)(g.pitch_t / kStep);
+        w.cols_b = g.pitch;
+        w.steps = (int)(up(n, kStep) / kStep);
         w.split = 1;
         w.most = most;
         w.scale = q->grad_scale / kBy;
@@ -1155,15 +1241,17 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       }
       // two products that leave compute units idle run side by side
       if (q->d_hidden && q->d_weight && for_h.tiles == kTiny && tiles_w == kTiny) {
-        product<E, TERMS, kGrads>(h, &w, kTiny, s);
+        const unsigned first = grid_of<Tiny>(h), second = grid_of<Tiny>(w);
+        hipLaunchKernelGGL((k_products<E, TERMS, Tiny>), dim3(first + second), dim3(kThreadsOf<Tiny>),
+                           0, s, h, w, (int)first);
       } else {
-        if (q->d_hidden) product<E, TERMS, kGrads>(h, nullptr, for_h.tiles, s);
-        if (q->d_weight) product<E, TERMS, kGrads>(w, nullptr, tiles_w, s);
+        if (q->d_hidden) product<E, TERMS, kGrads, true, false>(h, for_h.tiles, s);
+        if (q->d_weight) product<E, TERMS, kGrads, false, true>(w, tiles_w, s);
       }
     }
     if (q->d_hidden && split > 1)
       hipLaunchKernelGGL(k_join<T>, dim3(blocks(n * div_up(D, 8), p->cus)), dim3(256), 0, s,
-                         floats(l.sums), split, n, D, rows, q->grad_scale / kBy,
+                         floats(l.sums), split, n, D, rows, (bool)__is_same(T, f16_t), q->grad_scale / kBy,
                          static_cast<T*>(q->d_hidden) + r0 * q->d_hidden_stride, q->d_hidden_stride);
   }
 }
