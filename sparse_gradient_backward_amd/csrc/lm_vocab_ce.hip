@@ -40,18 +40,30 @@ constexpr float kUp = 32768.f;   // 2^15: see above; fp16 gradients are scaled b
 
 typedef float F4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ F4 mfma(Vec<bf16_t>::type a, Vec<bf16_t>::type b, F4 c) {
+// 16 bytes of an operand's row: a lane's part of a fragment.
+template <typename E>
+struct Frag {
+  typedef E type __attribute__((ext_vector_type(16 / sizeof(E))));
+};
+__device__ __forceinline__ F4 mfma(Frag<bf16_t>::type a, Frag<bf16_t>::type b, F4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ F4 mfma(Vec<f16_t>::type a, Vec<f16_t>::type b, F4 c) {
+__device__ __forceinline__ F4 mfma(Frag<f16_t>::type a, Frag<f16_t>::type b, F4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ F4 mfma(Frag<float>::type a, Frag<float>::type b, F4 c) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[k], b[k], c, 0, 0, 0);
+  return c;
 }
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ---------------------------------------------------------------- the product
 
-constexpr int kStep = 64;  // of the summed dimension: 128 bytes a row
-constexpr int kRowBytes = kStep * 2;
+constexpr int kRowBytes = 128;  // of the summed dimension a step
+template <typename E>
+constexpr int kStepOf = kRowBytes / (int)sizeof(E);
+constexpr int kPad = 64;        // and what it is rounded up to
 
 // A workgroup's tile of C (rows of A by rows of B), a wave's, and the steps that
 // are loaded between two barriers.
@@ -160,25 +172,57 @@ struct Stage {
 };
 
 // The same of an operand held the other way, the summed dimension from row to
-// row: 64 rows of R elements.  A matrix instruction's operand is read from it
-// transposed, 16 lanes at a time from four rows of 32 bytes; the rows' pieces of
-// 32 bytes are stored in an order that puts those of eight such rows into
-// different banks.
-template <int R>
-__device__ __forceinline__ int order_of(int row) {  // for rows of 128 bytes, two to a round of banks
-  return R > 64 ? (row & 3) | (row >> 3 & 1) << 2 : (row >> 1 & 1) | (row >> 3 & 1) << 1;
-}
-template <int R, int WAVES>
+// row: a step's rows of R elements.  Elements of 16 bits are read from it
+// transposed, 16 lanes at a time four rows of 32 bytes; of 32 bits one by one, 64
+// bytes from each of four rows.  The rows' pieces of such sizes are stored in an
+// order that puts those read at once into different banks.
+template <int R, typename E>
+struct Other {
+  static constexpr int kRow = R * (int)sizeof(E), kPiece = 16 * (int)sizeof(E);
+  static __device__ __forceinline__ int order(int row) {
+    if (sizeof(E) == 4) return row >> 2 & 3;
+    if (R > 64) return (row & 3) | (row >> 3 & 1) << 2;
+    return (row >> 1 & 1) | (row >> 3 & 1) << 1;  // two rows to a round of banks
+  }
+  // A lane's first element of 16 columns from `col` on (of 16), in its first row;
+  // those 16 i further are at ^ i * kPiece (col a multiple of as many as there are).
+  static __device__ __forceinline__ uint32_t at(int lane, int col) {
+    const int row = sizeof(E) == 4 ? 4 * (lane >> 4) : 8 * (lane >> 4) + (lane >> 2 & 3);
+    const int in = sizeof(E) == 4 ? (lane & 15) * 4 : (lane & 3) * 8;
+    return row * kRow + in + (col / 16 ^ order(row)) * kPiece;
+  }
+  static __device__ __forceinline__ typename Frag<E>::type read(const char* from) {
+    typename Frag<E>::type v{};
+#ifdef __HIP_DEVICE_COMPILE__
+    if constexpr (sizeof(E) == 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float*>(from + k * kRow);
+    } else {
+      typedef short H __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) H* P;
+      struct {
+        H lo, hi;
+      } h = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((P)from),
+             __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(from + 4 * kRow))};
+      v = __builtin_bit_cast(typename Frag<E>::type, h);
+    }
+#endif
+    return v;
+  }
+};
+template <int R, int WAVES, typename E>
 struct StageOther {
-  static constexpr int J = R / (8 * WAVES);
+  static constexpr int J = R / (8 * WAVES), kParts = R * (int)sizeof(E) / 16;
   uint32_t off[J];
   __device__ __forceinline__ void init(int wave, int lane, int64_t left, int64_t ld) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int at = (wave * J + j) * 64 + lane;  // 16 bytes each
-      const int row = at / (R / 8), part = at % (R / 8) ^ order_of<R>(row) << 1;
+      const int row = at / kParts;
+      const int part = at % kParts ^ Other<R, E>::order(row) * (Other<R, E>::kPiece / 16);
       // columns past the last are copies of others
-      off[j] = (uint32_t)row * (uint32_t)ld + (uint32_t)min((int64_t)part, left / 8 - 1) * 16;
+      off[j] = (uint32_t)row * (uint32_t)ld +
+               (uint32_t)min((int64_t)part, left * (int)sizeof(E) / 16 - 1) * 16;
     }
   }
   __device__ __forceinline__ void load(const char* base, char* lds, int wave) const {
@@ -277,11 +321,12 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % (TM / WM) * WM, wn = wave / (TM / WM) * WN;
 
-  typename std::conditional<AO, StageOther<TM, WAVES>, Stage<TM, WAVES>>::type sa;
-  typename std::conditional<BO, StageOther<TN, WAVES>, Stage<TN, WAVES>>::type sb;
+  typename std::conditional<AO, StageOther<TM, WAVES, E>, Stage<TM, WAVES>>::type sa;
+  typename std::conditional<BO, StageOther<TN, WAVES, E>, Stage<TN, WAVES>>::type sb;
   sa.init(wave, lane, (AO ? p.cols_a : p.M) - m0, p.lda);
   sb.init(wave, lane, (BO ? p.cols_b : p.N) - n0, p.ldb);
-  const char *a = p.a + m0 * (AO ? 2 : p.lda), *b = p.b + n0 * (BO ? 2 : p.ldb);
+  const char *a = p.a + m0 * (AO ? (int)sizeof(E) : p.lda);
+  const char* b = p.b + n0 * (BO ? (int)sizeof(E) : p.ldb);
   const int from = (int)((int64_t)p.steps * part / p.split);
   const int to = (int)((int64_t)p.steps * (part + 1) / p.split);
   const int steps = (to - from) * TERMS, turns = (steps + C::kSteps - 1) / C::kSteps;
@@ -291,8 +336,8 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
   const auto stage = [&](char* buf) {
 #pragma unroll
     for (int s = 0; s < C::kSteps; ++s) {
-      const char* pa = a + step * (AO ? kStep * p.lda : kRowBytes);
-      const char* pb = b + step * (BO ? kStep * p.ldb : kRowBytes);
+      const char* pa = a + step * (AO ? kStepOf<E> * p.lda : kRowBytes);
+      const char* pb = b + step * (BO ? kStepOf<E> * p.ldb : kRowBytes);
       if (TERMS > 1) {
         pa += (kPartsA >> (2 * term) & 3) * p.plane_a;
         pb += (kPartsB >> (2 * term) & 3) * p.plane_b;
@@ -312,27 +357,15 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = F4{0.f, 0.f, 0.f, 0.f};
 
-  // A step is two of 32, each with its fragments read while the one before
+  // A step is two halves, each with its fragments read while the one before
   // multiplies.  A turn's last products come after the barrier that frees its
   // buffer, and cover the next turn's first reads.
-  typedef typename Vec<E>::type V8;
-  V8 fa[2][FM], fb[2][FN];
+  typedef typename Frag<E>::type V;
+  typedef Other<TM, E> OA;
+  typedef Other<TN, E> OB;
+  V fa[2][FM], fb[2][FN];
   const int key = (lane >> 1) & 7, row = (lane & 15) * kRowBytes;
-  // held the other way: 4 of a lane's 8 elements from 4 rows by 16 columns
-  const auto other = [&](const char* at, int wide) -> V8 {
-    typedef short H __attribute__((ext_vector_type(4)));
-    struct {
-      H lo, hi;
-    } v{};
-#ifdef __HIP_DEVICE_COMPILE__
-    v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) H*)at);
-    v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) H*)(at + 4 * wide));
-#endif
-    return __builtin_bit_cast(V8, v);
-  };
-  const int r4 = 8 * (lane >> 4) + (lane >> 2 & 3);  // this lane's first row of a step of 32
-  const uint32_t at_a = r4 * TM * 2 + (lane & 3) * 8 + (wm / 16 ^ order_of<TM>(r4)) * 32;
-  const uint32_t at_b = r4 * TN * 2 + (lane & 3) * 8 + (wn / 16 ^ order_of<TN>(r4)) * 32;
+  const uint32_t at_a = OA::at(lane, wm), at_b = OB::at(lane, wn);
   const auto read = [&](const char* buf, int kk) {
     const int at = row + ((kk * 4 + (lane >> 4)) ^ key) * 16;
     // (one address a fragment, made when it is needed: kept, they would spill)
@@ -342,22 +375,24 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       if constexpr (BO)
-        fb[kk][j] = other(buf + (TM * kRowBytes + kk * 32 * TN * 2 + (ob ^ j * 32)), TN * 2);
+        fb[kk][j] = OB::read(buf + (TM * kRowBytes + kk * kStepOf<E> / 2 * OB::kRow + (ob ^ j * OB::kPiece)));
       else
-        fb[kk][j] = *reinterpret_cast<const V8*>(buf + (uint32_t)((TM + wn) * kRowBytes + at + j * 16 * kRowBytes));
+        fb[kk][j] = *reinterpret_cast<const V*>(buf + (uint32_t)((TM + wn) * kRowBytes + at + j * 16 * kRowBytes));
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       if constexpr (AO)
-        fa[kk][i] = other(buf + (kk * 32 * TM * 2 + (oa ^ i * 32)), TM * 2);
+        fa[kk][i] = OA::read(buf + (kk * kStepOf<E> / 2 * OA::kRow + (oa ^ i * OA::kPiece)));
       else
-        fa[kk][i] = *reinterpret_cast<const V8*>(buf + (uint32_t)(wm * kRowBytes + at + i * 16 * kRowBytes));
+        fa[kk][i] = *reinterpret_cast<const V*>(buf + (uint32_t)(wm * kRowBytes + at + i * 16 * kRowBytes));
     }
   };
   const auto multiply = [&](int kk) {
     // Products and reads in turn.  The first products come before any read: they
     // free their operands' registers for it.
-    constexpr int kReads = FM * (1 + AO) + FN * (1 + BO), kAll = FM * FN;
+    constexpr int kApart = sizeof(E) == 4 ? 4 : 2;  // reads of a fragment held the other way
+    constexpr int kReads = FM * (AO ? kApart : 1) + FN * (BO ? kApart : 1);
+    constexpr int kAll = FM * FN * (sizeof(E) == 4 ? 4 : 1);
     constexpr int kLead = kAll > kReads ? kAll - kReads < 8 ? kAll - kReads : 8 : 0;
     constexpr int kEach = kAll - kLead < kReads ? 1 : (kAll - kLead) / kReads;
 #pragma unroll
@@ -556,16 +591,16 @@ __global__ __launch_bounds__(kThreadsOf<C>, 2) void k_products(Product h, Produc
 
 // ---------------------------------------------------------------- copies
 
-// What an operand's element becomes: itself, or the three bf16 parts of an
+// What an operand's element becomes: itself, or (SPLIT) the three bf16 parts of an
 // fp32 number, each what the ones before it leave (exact but for subnormals).
-template <typename T>
+template <typename T, bool SPLIT>
 struct Parts {
   static constexpr int kCount = 1;
   typedef T E;
   static __device__ __forceinline__ void split(T v, E (&out)[1]) { out[0] = v; }
 };
 template <>
-struct Parts<float> {
+struct Parts<float, true> {
   static constexpr int kCount = 3;
   typedef bf16_t E;
   static __device__ __forceinline__ void split(float v, E (&out)[3]) {
@@ -579,21 +614,24 @@ struct Parts<float> {
   }
 };
 
-template <typename T, typename V>
-__device__ __forceinline__ void store_parts(const V (&v)[8], typename Parts<T>::E* to, int64_t plane) {
-  typedef typename Parts<T>::E E;
-  constexpr int P = Parts<T>::kCount;
-  E out[P][8];
+template <typename T, bool SPLIT, typename V>
+__device__ __forceinline__ void store_parts(const V (&v)[8], typename Parts<T, SPLIT>::E* to,
+                                            int64_t plane) {
+  typedef typename Parts<T, SPLIT>::E E;
+  constexpr int P = Parts<T, SPLIT>::kCount;
+  __attribute__((aligned(16))) E out[P][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     E e[P];
-    Parts<T>::split((T)v[i], e);
+    Parts<T, SPLIT>::split((T)v[i], e);
 #pragma unroll
     for (int k = 0; k < P; ++k) out[k][i] = e[k];
   }
 #pragma unroll
   for (int k = 0; k < P; ++k)
-    *reinterpret_cast<uint4*>(to + k * plane) = *reinterpret_cast<const uint4*>(out[k]);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(E) / 2; ++i)
+      reinterpret_cast<uint4*>(to + k * plane)[i] = reinterpret_cast<const uint4*>(out[k])[i];
 }
 
 constexpr int kTile = 64;
@@ -602,9 +640,9 @@ constexpr int kTile = 64;
 // zeros past D and past the last row; transposed to [D][pitch_t] with zeros past
 // the last row and in rows that do not count (what they hold may be no number);
 // or both.
-template <typename T>
+template <typename T, bool SPLIT>
 struct Copy {
-  typedef typename Parts<T>::E E;
+  typedef typename Parts<T, SPLIT>::E E;
   const T* src;
   int64_t stride, rows;
   int D;
@@ -614,8 +652,8 @@ struct Copy {
 };
 
 // Tiles of 64 x 64, of `a` in the first workgroups and of `b` in the others.
-template <typename T>
-__global__ __launch_bounds__(256) void k_copy(Copy<T> a, Copy<T> b, unsigned first) {
+template <typename T, bool SPLIT>
+__global__ __launch_bounds__(256) void k_copy(Copy<T, SPLIT> a, Copy<T, SPLIT> b, unsigned first) {
   __shared__ __attribute__((aligned(16))) T tile[kTile][kTile + 4 / sizeof(T)];
   unsigned block = blockIdx.x;
   if (block >= first) {
@@ -634,7 +672,7 @@ __global__ __launch_bounds__(256) void k_copy(Copy<T> a, Copy<T> b, unsigned fir
     if (a.to) {
       T v[8];
       __builtin_memcpy(v, &raw, sizeof v);
-      store_parts<T>(v, a.to + (r0 + r) * a.pitch + d0 + c, a.plane);
+      store_parts<T, SPLIT>(v, a.to + (r0 + r) * a.pitch + d0 + c, a.plane);
     }
     if (!a.to_t) continue;
     const bool on = there && factor_of(a.count, r0 + r) != 0.f;
@@ -651,7 +689,7 @@ __global__ __launch_bounds__(256) void k_copy(Copy<T> a, Copy<T> b, unsigned fir
     T v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = tile[c + i][d];
-    store_parts<T>(v, a.to_t + (int64_t)(d0 + d) * a.pitch_t + r0 + c, a.plane_t);
+    store_parts<T, SPLIT>(v, a.to_t + (int64_t)(d0 + d) * a.pitch_t + r0 + c, a.plane_t);
   }
 }
 
@@ -754,9 +792,9 @@ struct Grad {
 
 // The gradient of a piece's logits from their exponentials, in the operands'
 // type, zeros past the vocabulary and past the last token.
-template <typename T, typename X, bool SUM>
+template <typename T, bool SPLIT, typename X, bool SUM>
 __global__ __launch_bounds__(256) void k_grad(Grad q) {
-  typedef typename Parts<T>::E E;
+  typedef typename Parts<T, SPLIT>::E E;
   constexpr float kBy = __is_same(T, f16_t) ? kUp : 1.f;  // fp16 has no room below 2^-24
   __shared__ float2 part[SUM ? kShares : 1][SUM ? kTile : 1];
   const unsigned across = (unsigned)(q.pitch / kTile);
@@ -826,11 +864,11 @@ __global__ __launch_bounds__(256) void k_grad(Grad q) {
     for (int i = 0; i < 8; ++i)
       v[i] = on && i < n ? (e[i] * k - (label[u] == i ? 1.f : 0.f)) * kBy : 0.f;
     const int64_t to = (r0 + lr) * q.pitch + c0 + c;
-    if (q.plain) store_parts<T>(v, static_cast<E*>(q.plain) + to, q.plane);
+    if (q.plain) store_parts<T, SPLIT>(v, static_cast<E*>(q.plain) + to, q.plane);
     if (q.scaled) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= share;
-      store_parts<T>(v, static_cast<E*>(q.scaled) + to, q.plane);
+      store_parts<T, SPLIT>(v, static_cast<E*>(q.scaled) + to, q.plane);
     }
   }
 }
@@ -906,30 +944,34 @@ int wave_cols_of(Tiles t) { return t == kBig ? Big::WM : t == kMedium ? Medium::
 struct Choice {
   Tiles tiles;
   int split;
+  double us;
 };
-Choice choose(int64_t M, int64_t N, int64_t steps, int terms, int cus, int most) {
-  struct {
-    int64_t tiles;
-    int slots;
-    double step, rest;
-  } const kinds[] = {{tiles_of<Big>(M, N), cus, 1.65, 8.0},
-                     {tiles_of<Medium>(M, N), 2 * cus, 1.05, 2.0},
-                     {tiles_of<Tiny>(M, N), cus, 0.39, 4.0}};
-  Choice best{kBig, 1};
-  double least = 1e300;
+// 16-bit operands, fp32 in parts (six products of 16 bits), fp32 as it is.
+enum Rate { kHalf, kSplit, kWhole };
+Choice choose(int64_t M, int64_t N, int64_t K, Rate rate, int cus, int most) {
+  const double per64[3][3] = {{1.65, 1.05, 0.39}, {9.9, 6.3, 2.34}, {14.0, 7.0, 1.0}};
+  const double rest[3] = {8.0, 2.0, 4.0};
+  const int64_t tiles[3] = {tiles_of<Big>(M, N), tiles_of<Medium>(M, N), tiles_of<Tiny>(M, N)};
+  const int slots[3] = {cus, 2 * cus, cus};
+  const int64_t steps = K / kPad;
+  Choice best{kBig, 1, 1e300};
   for (int t = 0; t < 3; ++t)
     for (int split = 1; split <= most && split <= steps; split *= 2) {
-      const auto& k = kinds[t];
-      if (split > 1 && k.tiles * split > 2 * cus) break;
-      double us = (double)div_up(k.tiles * split, k.slots) *
-                  ((double)div_up(steps, split) * terms * k.step + k.rest);
+      if (split > 1 && tiles[t] * split > 2 * cus) break;
+      double us = (double)div_up(tiles[t] * split, slots[t]) *
+                  ((double)div_up(steps, split) * per64[rate][t] + rest[t]);
       if (split > 1) us += 4 + 2e-6 * (double)(M * N) * split;  // the sums written and read
-      if (us < least) {
-        least = us;
-        best = {(Tiles)t, split};
-      }
+      if (us < best.us) best = {(Tiles)t, split, us};
     }
   return best;
+}
+
+// fp32 operands in parts take less of the matrix units and have to be copied, at
+// 10 bytes an element and 4.5 TB/s: for few rows the copy costs more.
+bool in_parts(const sgb_vocab_ce_s* p, int64_t rows) {
+  const double copy = (double)p->V * p->D * 10 / 4.5e6;
+  const int64_t K = up(p->D, kPad);
+  return choose(p->V, rows, K, kSplit, p->cus, 1).us + copy < choose(p->V, rows, K, kWhole, p->cus, 1).us;
 }
 
 // What a call lays out in its workspace.
@@ -945,13 +987,13 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   Layout l{};
   l.parts = dtype == SGB_F32 ? 3 : 1;
   const int64_t V = p->V, D = p->D, exp_size = dtype == SGB_BF16 ? 2 : 4;
-  l.pitch_d = up(D, kStep);
+  l.pitch_d = up(D, kPad);
   l.ld_exps = up(V, 256);  // whole tiles
   int64_t most = kStatBytes / (l.ld_exps / Tiny::WM * 8);
   if (gradient) most = std::min(most, kExpBytes / (l.ld_exps * exp_size));
   most = std::max<int64_t>(most / 256 * 256, 64);
   l.chunk = std::min(rows, most);
-  l.pad = up(l.chunk, kStep);
+  l.pad = up(l.chunk, kPad);
   const int64_t room = kPieceElems / l.parts;
   l.piece = std::min(l.ld_exps,
                      std::max<int64_t>(256, std::min(room / l.pad, room / l.pitch_d) / 256 * 256));
@@ -1015,26 +1057,27 @@ struct Operand {
   int64_t ld, plane;  // bytes
 };
 
-template <typename T>
+template <typename T, bool SPLIT>
 struct Copies {  // asked for, to be launched together
-  Copy<T> c[2];
+  Copy<T, SPLIT> c[2];
   int n = 0;
-  static unsigned tiles(const Copy<T>& c) {
+  static unsigned tiles(const Copy<T, SPLIT>& c) {
     return (unsigned)(div_up(c.rows, kTile) * div_up(c.D, kTile));
   }
   void launch(hipStream_t s) {
     if (n == 0) return;
     const unsigned first = tiles(c[0]), second = n > 1 ? tiles(c[1]) : 0;
-    hipLaunchKernelGGL(k_copy<T>, dim3(first + second), dim3(256), 0, s, c[0], c[n - 1], first);
+    hipLaunchKernelGGL((k_copy<T, SPLIT>), dim3(first + second), dim3(256), 0, s, c[0], c[n - 1], first);
     n = 0;
   }
 };
 
-template <typename T>
+template <typename T, bool SPLIT = false>
 void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const Layout& l, char* ws,
              hipStream_t s) {
-  typedef typename Parts<T>::E E;
-  constexpr int TERMS = Parts<T>::kCount == 3 ? 6 : 1;
+  typedef typename Parts<T, SPLIT>::E E;
+  constexpr int TERMS = SPLIT ? 6 : 1, ES = sizeof(E);
+  constexpr Rate RATE = SPLIT ? kSplit : ES == 4 ? kWhole : kHalf;
   typedef typename std::conditional<__is_same(T, bf16_t), f16_t, float>::type X;
   constexpr float kBy = __is_same(T, f16_t) ? kUp : 1.f;
   const int64_t R = q->rows, V = p->V;
@@ -1056,29 +1099,29 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
   // Rows as the products read them: whole 128-byte lines, 16-byte aligned, a
   // tile's within 32 bits.
   const auto fits = [&](const void* a, int64_t stride, int64_t rows) {
-    return sizeof(T) == 2 && D % kStep == 0 && aligned(a, 16) &&
-           (rows < 2 || (stride % 8 == 0 && stride < (1 << 22)));
+    return !SPLIT && D % kPad == 0 && aligned(a, 16) &&
+           (rows < 2 || (stride * ES % 16 == 0 && stride * ES < (1 << 23)));
   };
   const bool weight_fits = fits(weight, q->weight_stride, V);
-  Copies<T> copies;
+  Copies<T, SPLIT> copies;
   const auto copy_of = [&](const T* src, int64_t stride, int64_t n) {
-    Copy<T> c{src, stride, n, D};
+    Copy<T, SPLIT> c{src, stride, n, D};
     c.pitch = l.pitch_d;
-    c.plane = up(n, kStep) * c.pitch;
-    c.pitch_t = up(n, kStep);
+    c.plane = up(n, kPad) * c.pitch;
+    c.pitch_t = up(n, kPad);
     c.plane_t = D * c.pitch_t;
     return c;
   };
-  const auto operand = [](const E* p, const Copy<T>& c) {
-    return Operand{reinterpret_cast<const char*>(p), c.pitch * 2, c.plane * 2};
+  const auto operand = [](const E* p, const Copy<T, SPLIT>& c) {
+    return Operand{reinterpret_cast<const char*>(p), c.pitch * ES, c.plane * ES};
   };
   // A piece of the weight; whole: its rows are read by whole steps, past the
   // vocabulary where that is not one of steps.
   const auto weight_rows = [&](int64_t v0, int64_t width, bool whole) {
     const T* src = weight + v0 * q->weight_stride;
-    if (weight_fits && !(whole && v0 + width == V && V % kStep != 0))
-      return Operand{reinterpret_cast<const char*>(src), q->weight_stride * 2, 0};
-    Copy<T> c = copy_of(src, q->weight_stride, width);
+    if (weight_fits && !(whole && v0 + width == V && V % kPad != 0))
+      return Operand{reinterpret_cast<const char*>(src), q->weight_stride * ES, 0};
+    Copy<T, SPLIT> c = copy_of(src, q->weight_stride, width);
     c.to = elems(l.w);
     copies.c[copies.n++] = c;
     return operand(c.to, c);
@@ -1091,8 +1134,8 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     const int64_t n = std::min(l.chunk, R - r0);
     const Rows rows = rows_at(r0);
     const T* x = static_cast<const T*>(q->hidden) + r0 * q->hidden_stride;
-    Copy<T> c = copy_of(x, q->hidden_stride, n);
-    Operand xo{reinterpret_cast<const char*>(x), q->hidden_stride * 2, 0}, xt{}, wo{};
+    Copy<T, SPLIT> c = copy_of(x, q->hidden_stride, n);
+    Operand xo{reinterpret_cast<const char*>(x), q->hidden_stride * ES, 0}, xt{}, wo{};
     if (!fits(x, q->hidden_stride, n)) {
       c.to = elems(l.x);
       xo = operand(c.to, c);
@@ -1100,7 +1143,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     if (grad && q->d_weight) {
       c.to_t = elems(l.xt);
       c.count = rows;
-      xt = {reinterpret_cast<const char*>(c.to_t), c.pitch_t * 2, c.plane_t * 2};
+      xt = {reinterpret_cast<const char*>(c.to_t), c.pitch_t * ES, c.plane_t * ES};
     }
     if (c.to || c.to_t) copies.c[copies.n++] = c;
     Product a{};
@@ -1108,7 +1151,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     a.ldb = xo.ld;
     a.plane_b = xo.plane;
     a.N = a.tokens = n;
-    a.steps = (int)(l.pitch_d / kStep);
+    a.steps = (int)(l.pitch_d / kStepOf<E>);
     a.split = 1;
     a.rows = rows;
     a.stats = reinterpret_cast<float2*>(ws + l.stats);
@@ -1117,7 +1160,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     a.exps = ws + l.exps;
     a.ld_exps = l.ld_exps;
     // (one kind of tile for all pieces: they share the rows of sums)
-    const Tiles tiles = choose(std::min(logits_piece, V), n, a.steps, TERMS, p->cus, 1).tiles;
+    const Tiles tiles = choose(std::min(logits_piece, V), n, l.pitch_d, RATE, p->cus, 1).tiles;
     for (int64_t v0 = 0; v0 < V; v0 += logits_piece) {
       const int64_t width = std::min(logits_piece, V - v0);
       // (a single piece's copy serves d_hidden as well)
@@ -1152,7 +1195,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     if (!gradients) continue;
 
     // (of the first piece, the longest, which writes every part's sums)
-    const Choice for_h = choose(D, n, div_up(std::min(l.piece, V), kStep), TERMS, p->cus, kMaxSplit);
+    const Choice for_h = choose(D, n, up(std::min(l.piece, V), kPad), RATE, p->cus, kMaxSplit);
     const int split = for_h.split;
     for (int64_t v0 = 0; v0 < V; v0 += l.piece) {
       const int64_t width = std::min(l.piece, V - v0);
@@ -1165,18 +1208,18 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       g.most = most;
       g.v0 = v0;
       g.width = width;
-      g.pitch = up(width, kStep);
-      g.plane = up(n, kStep) * g.pitch;
+      g.pitch = up(width, kPad);
+      g.plane = up(n, kPad) * g.pitch;
       // Both products take the gradient with the row's factor; but fp16 could not
       // hold that of a small one, and d_hidden takes it without.
       constexpr bool kTwo = __is_same(T, f16_t);
       if (q->d_weight || !kTwo) g.scaled = ws + l.scaled;
       if (q->d_hidden && kTwo) g.plain = ws + l.plain;
-      const dim3 grid((unsigned)(g.pitch / kStep * (up(n, kStep) / kStep)));
+      const dim3 grid((unsigned)(g.pitch / kPad * (up(n, kPad) / kPad)));
       if (sum_later)
-        hipLaunchKernelGGL((k_grad<T, X, true>), grid, dim3(256), 0, s, g);
+        hipLaunchKernelGGL((k_grad<T, SPLIT, X, true>), grid, dim3(256), 0, s, g);
       else
-        hipLaunchKernelGGL((k_grad<T, X, false>), grid, dim3(256), 0, s, g);
+        hipLaunchKernelGGL((k_grad<T, SPLIT, X, false>), grid, dim3(256), 0, s, g);
       Product h{}, w{};
       if (q->d_hidden) {
         if (!one_piece) {
@@ -1187,12 +1230,12 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
         h.lda = wo.ld;
         h.plane_a = wo.plane;
         h.b = static_cast<const char*>(kTwo ? g.plain : g.scaled);
-        h.ldb = g.pitch * 2;
-        h.plane_b = g.plane * 2;
+        h.ldb = g.pitch * ES;
+        h.plane_b = g.plane * ES;
         h.M = D;
         h.cols_a = l.pitch_d;
         h.N = n;
-        h.steps = (int)(g.pitch / kStep);
+        h.steps = (int)(g.pitch / kStepOf<E>);
         h.split = std::min(split, h.steps);
         if (split == 1 && v0 + width == V) {
           h.rows = rows;
@@ -1211,17 +1254,17 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       if (q->d_weight) {
         const bool first = r0 == 0, last = r0 + n == R;
         const bool direct = (first && last) || q->d_weight_dtype == SGB_F32;
-        tiles_w = choose(D, width, up(n, kStep) / kStep, TERMS, p->cus, 1).tiles;
+        tiles_w = choose(D, width, up(n, kPad), RATE, p->cus, 1).tiles;
         w.a = xt.p;
         w.lda = xt.ld;
         w.plane_a = xt.plane;
         w.b = static_cast<const char*>(g.scaled);
-        w.ldb = g.pitch * 2;
-        w.plane_b = g.plane * 2;
+        w.ldb = g.pitch * ES;
+        w.plane_b = g.plane * ES;
         w.M = D;
         w.N = width;
         w.cols_b = g.pitch;
-        w.steps = (int)(up(n, kStep) / kStep);
+        w.steps = (int)(up(n, kPad) / kStepOf<E>);
         w.split = 1;
         w.most = most;
         w.scale = q->grad_scale / kBy;
@@ -1307,7 +1350,10 @@ sgb_status call(sgb_vocab_ce p, const sgb_vocab_ce_args* q, Way way, void* ws, s
     : q->dtype == SGB_BF16       ? zero<bf16_t>(p, q, s)
                                  : zero<f16_t>(p, q, s);
   } else if (q->dtype == SGB_F32) {
-    enqueue<float>(p, q, way, l, static_cast<char*>(ws), s);
+    if (in_parts(p, std::min(R, l.chunk)))
+      enqueue<float, true>(p, q, way, l, static_cast<char*>(ws), s);
+    else
+      enqueue<float>(p, q, way, l, static_cast<char*>(ws), s);
   } else if (q->dtype == SGB_BF16) {
     enqueue<bf16_t>(p, q, way, l, static_cast<char*>(ws), s);
   } else {
