@@ -51,10 +51,8 @@ __device__ __forceinline__ F4 mfma(Frag<bf16_t>::type a, Frag<bf16_t>::type b, F
 __device__ __forceinline__ F4 mfma(Frag<f16_t>::type a, Frag<f16_t>::type b, F4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ F4 mfma(Frag<float>::type a, Frag<float>::type b, F4 c) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[k], b[k], c, 0, 0, 0);
-  return c;
+__device__ __forceinline__ F4 mfma(float a, float b, F4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -78,6 +76,12 @@ struct Medium {  // two, one at its start or end while the other multiplies
 };
 struct Tiny {  // for the time that loads take, not for how many there are
   static constexpr int TM = 64, TN = 64, WM = 32, WN = 32, kSteps = 4;
+};
+struct Thin {  // few of B's rows: what bounds it is A's being read
+  static constexpr int TM = 256, TN = 16, WM = 64, WN = 16, kSteps = 1;
+};
+struct Brief {  // few steps: the result's being written; four a compute unit, one buffer each
+  static constexpr int TM = 128, TN = 128, WM = 64, WN = 64, kSteps = 1;
 };
 template <typename C>
 constexpr int kThreadsOf = C::TM / C::WM * (C::TN / C::WN) * 64;
@@ -155,19 +159,20 @@ __device__ __forceinline__ void load_to_lds(const char* base, const uint32_t (&o
 // consecutive over the lanes, so the order is made by what a lane loads.
 template <int R, int WAVES>
 struct Stage {
-  static constexpr int J = R / (8 * WAVES);
+  // (where there are fewer loads than waves, some waves make the same one)
+  static constexpr int kLoads = R / 8, J = kLoads < WAVES ? 1 : kLoads / WAVES;
   uint32_t off[J];
   __device__ __forceinline__ void init(int wave, int lane, int64_t left, int64_t ld) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int row = (wave * J + j) * 8 + (lane >> 3);
+      const int row = (wave * J % kLoads + j) * 8 + (lane >> 3);
       const int part = (lane & 7) ^ ((row >> 1) & 7);
       // rows past the last are copies of it: nothing is read out of range
       off[j] = (uint32_t)min((int64_t)row, left - 1) * (uint32_t)ld + part * 16;
     }
   }
   __device__ __forceinline__ void load(const char* base, char* lds, int wave) const {
-    load_to_lds(base, off, lds + wave * (J * 1024));
+    load_to_lds(base, off, lds + wave * J % kLoads * 1024);
   }
 };
 
@@ -395,10 +400,18 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
     constexpr int kAll = FM * FN * (sizeof(E) == 4 ? 4 : 1);
     constexpr int kLead = kAll > kReads ? kAll - kReads < 8 ? kAll - kReads : 8 : 0;
     constexpr int kEach = kAll - kLead < kReads ? 1 : (kAll - kLead) / kReads;
+    constexpr int kEvery = sizeof(E) == 4 ? 4 : 1;  // (fp32: four, far apart: each waits for the one before)
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int k = 0; k < kEvery; ++k)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = mfma(fa[kk][i], fb[kk][j], acc[i][j]);
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (sizeof(E) == 4)
+            acc[i][j] = mfma(fa[kk][i][k], fb[kk][j][k], acc[i][j]);
+          else
+            acc[i][j] = mfma(fa[kk][i], fb[kk][j], acc[i][j]);
+        }
     if (kLead) __builtin_amdgcn_sched_group_barrier(0x008, kLead, 0);
 #pragma unroll
     for (int i = 0; i < kReads && i < kAll; ++i) {
@@ -424,43 +437,58 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
   };
 
   stage(buf0);
-  stage(buf1);
-  all_loaded();
-  read(buf0, 0);
-  int left = turns;
-  for (; left > 2; left -= 2) {
-    turn(buf0);
-    all_loaded();
-    stage(buf0);
-    read(buf1, 0);
-    multiply(1);
-    turn(buf1);
-    all_loaded();
+  if constexpr (__is_same(C, Brief)) {
+    for (int s = 1;; ++s) {
+      all_loaded();
+      read(buf0, 0);
+      multiply(0);
+      read(buf0, 1);
+      multiply(1);
+      if (s >= turns) break;
+      __syncthreads();
+      stage(buf0);
+    }
+  } else {
     stage(buf1);
-    read(buf0, 0);
-    multiply(1);
-  }
-  if (left > 1) {
-    turn(buf0);
     all_loaded();
-    read(buf1, 0);
-    multiply(1);
-  }
-  const char* buf = left > 1 ? buf1 : buf0;
-  most(buf);
-  for (int s = (turns - 1) * C::kSteps + 1; s < steps; ++s) {  // (none where a turn is one step)
-    buf += kBytes;
-    read(buf, 0);
-    multiply(1);
+    read(buf0, 0);
+    int left = turns;
+    for (; left > 2; left -= 2) {
+      turn(buf0);
+      all_loaded();
+      stage(buf0);
+      read(buf1, 0);
+      multiply(1);
+      turn(buf1);
+      all_loaded();
+      stage(buf1);
+      read(buf0, 0);
+      multiply(1);
+    }
+    if (left > 1) {
+      turn(buf0);
+      all_loaded();
+      read(buf1, 0);
+      multiply(1);
+    }
+    const char* buf = left > 1 ? buf1 : buf0;
     most(buf);
+    for (int s = (turns - 1) * C::kSteps + 1; s < steps; ++s) {  // (none where a turn is one step)
+      buf += kBytes;
+      read(buf, 0);
+      multiply(1);
+      most(buf);
+    }
+    multiply(1);
   }
-  multiply(1);
   all_loaded();  // LDS is free: no load to it is under way any more
 
   // acc[i][j][k]: C's row (of A) m0 + wm + 16 i + 4 (lane / 16) + k, its column
   // (of B) n0 + wn + 16 j + lane % 16
   const int64_t mw = m0 + wm + 4 * (lane >> 4);
-  char* own = (wave < WAVES / 2 ? buf0 : buf1) + wave % (WAVES / 2) * Rows16<float, 4>::kBytes;
+  char* own = __is_same(C, Brief) ? buf0 + wave * Rows16<float, 4>::kBytes
+                                  : (wave < WAVES / 2 ? buf0 : buf1) +
+                                        wave % (WAVES / 2) * Rows16<float, 4>::kBytes;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     __builtin_amdgcn_sched_barrier(0);  // (all at once would spill)
@@ -573,8 +601,9 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
 // (buf0, buf1: variables of their own, so that a read of one does not wait for
 // loads to the other)
 template <typename E, int TERMS, int EPI, typename C, bool AO, bool BO>
-__global__ __launch_bounds__(kThreadsOf<C>, 2) void k_product(Product p) {
-  __shared__ __attribute__((aligned(1024))) char buf0[kBufBytes<C>], buf1[kBufBytes<C>];
+__global__ __launch_bounds__(kThreadsOf<C>, __is_same(C, Brief) ? 4 : 2) void k_product(Product p) {
+  __shared__ __attribute__((aligned(1024))) char buf0[kBufBytes<C>];
+  __shared__ __attribute__((aligned(1024))) char buf1[__is_same(C, Brief) ? 16 : kBufBytes<C>];
   product_tile<E, TERMS, EPI, C, AO, BO>(p, (int)blockIdx.x, buf0, buf1);
 }
 
@@ -760,18 +789,20 @@ __device__ __forceinline__ void finish_row(const Loss& q, int64_t r, float lse) 
 constexpr int kFewParts = 64;  // sums of a row that k_grad adds up itself
 constexpr int kShares = 16;  // of a row's sums, each added up alone and then in turn
 
-// 16 rows a workgroup.
+// 256 / SHARES rows a workgroup.
+template <int SHARES>
 __global__ __launch_bounds__(256) void k_lse(Loss q) {
-  __shared__ float2 all[kShares][17];
-  const int who = (int)threadIdx.x & 15, share = (int)threadIdx.x >> 4;
-  const int64_t r = (int64_t)blockIdx.x * 16 + who;
+  constexpr int kRows = 256 / SHARES;
+  __shared__ float2 all[SHARES][kRows + 1];
+  const int who = (int)threadIdx.x % kRows, share = (int)threadIdx.x / kRows;
+  const int64_t r = (int64_t)blockIdx.x * kRows + who;
   Sum mine;
-  if (r < q.tokens) mine.add_all(q.stats, q.parts, q.tokens, r, share, kShares);
+  if (r < q.tokens) mine.add_all(q.stats, q.parts, q.tokens, r, share, SHARES);
   all[share][who] = make_float2(mine.m, mine.s);
   __syncthreads();
-  if (threadIdx.x < 16 && r < q.tokens) {
+  if (threadIdx.x < kRows && r < q.tokens) {
     Sum sum;
-    for (int i = 0; i < kShares; ++i) sum.add(all[i][who]);
+    for (int i = 0; i < SHARES; ++i) sum.add(all[i][who]);
     finish_row(q, r, sum.log());
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) q.hdr->epoch = q.epoch;
@@ -930,8 +961,8 @@ int64_t tiles_of(int64_t M, int64_t N) {
   return div_up(M, C::TM) * div_up(N, C::TN);
 }
 
-enum Tiles { kBig, kMedium, kTiny };
-int wave_cols_of(Tiles t) { return t == kBig ? Big::WM : t == kMedium ? Medium::WM : Tiny::WM; }
+enum Tiles { kBig, kMedium, kTiny, kThin, kBrief };
+int wave_cols_of(Tiles t) { return t == kBig ? Big::WM : t == kTiny ? Tiny::WM : Medium::WM; }
 
 // The tiles of a product, and among how many workgroups each tile's summed
 // dimension is shared out (up to `most`; their sums are then joined): what takes
@@ -948,14 +979,15 @@ struct Choice {
 };
 // 16-bit operands, fp32 in parts (six products of 16 bits), fp32 as it is.
 enum Rate { kHalf, kSplit, kWhole };
-Choice choose(int64_t M, int64_t N, int64_t K, Rate rate, int cus, int most) {
-  const double per64[3][3] = {{1.65, 1.05, 0.39}, {9.9, 6.3, 2.34}, {14.0, 7.0, 1.0}};
-  const double rest[3] = {8.0, 2.0, 4.0};
-  const int64_t tiles[3] = {tiles_of<Big>(M, N), tiles_of<Medium>(M, N), tiles_of<Tiny>(M, N)};
-  const int slots[3] = {cus, 2 * cus, cus};
+Choice choose(int64_t M, int64_t N, int64_t K, Rate rate, int cus, int most, bool thin) {
+  const double per64[3][4] = {{1.65, 1.05, 0.39, 0.6}, {9.9, 6.3, 2.34, 3.6}, {14.0, 7.0, 1.0, 1.8}};
+  const double rest[4] = {8.0, 2.0, 4.0, 3.0};
+  const int64_t tiles[4] = {tiles_of<Big>(M, N), tiles_of<Medium>(M, N), tiles_of<Tiny>(M, N),
+                            tiles_of<Thin>(M, N)};
+  const int slots[4] = {cus, 2 * cus, cus, 2 * cus};
   const int64_t steps = K / kPad;
   Choice best{kBig, 1, 1e300};
-  for (int t = 0; t < 3; ++t)
+  for (int t = 0; t < (thin && N <= Thin::TN ? 4 : 3); ++t)
     for (int split = 1; split <= most && split <= steps; split *= 2) {
       if (split > 1 && tiles[t] * split > 2 * cus) break;
       double us = (double)div_up(tiles[t] * split, slots[t]) *
@@ -971,14 +1003,15 @@ Choice choose(int64_t M, int64_t N, int64_t K, Rate rate, int cus, int most) {
 bool in_parts(const sgb_vocab_ce_s* p, int64_t rows) {
   const double copy = (double)p->V * p->D * 10 / 4.5e6;
   const int64_t K = up(p->D, kPad);
-  return choose(p->V, rows, K, kSplit, p->cus, 1).us + copy < choose(p->V, rows, K, kWhole, p->cus, 1).us;
+  return choose(p->V, rows, K, kSplit, p->cus, 1, true).us + copy < choose(p->V, rows, K, kWhole, p->cus, 1, true).us;
 }
 
 // What a call lays out in its workspace.
 struct Layout {
   int parts;           // of an element
   int64_t chunk, pad;  // rows a chunk, rounded up for the summed dimension
-  int64_t piece;       // of the vocabulary
+  int64_t piece;       // of the vocabulary, where its rows are copied
+  int64_t room;        // elements of a piece's gradients
   int64_t pitch_d, ld_exps;
   size_t lse, said, most, stats, x, xt, w, exps, plain, scaled, sums, dw, bytes;
 };
@@ -994,7 +1027,7 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   most = std::max<int64_t>(most / 256 * 256, 64);
   l.chunk = std::min(rows, most);
   l.pad = up(l.chunk, kPad);
-  const int64_t room = kPieceElems / l.parts;
+  const int64_t room = l.room = kPieceElems / l.parts;
   l.piece = std::min(l.ld_exps,
                      std::max<int64_t>(256, std::min(room / l.pad, room / l.pitch_d) / 256 * 256));
   size_t at = kHeaderBytes;
@@ -1035,15 +1068,24 @@ unsigned grid_of(Product& p) {
 
 template <typename E, int TERMS, int EPI, bool AO = false, bool BO = false>
 void product(Product p, Tiles tiles, hipStream_t s) {
+  if (TERMS == 1 && tiles == kMedium && p.steps <= 4) tiles = kBrief;
   if (tiles == kBig)
     hipLaunchKernelGGL((k_product<E, TERMS, EPI, typename std::conditional<AO, BigOther, Big>::type, AO, BO>),
                        dim3(grid_of<Big>(p)), dim3(kThreadsOf<Big>), 0, s, p);
   else if (tiles == kMedium)
     hipLaunchKernelGGL((k_product<E, TERMS, EPI, Medium, AO, BO>), dim3(grid_of<Medium>(p)),
                        dim3(kThreadsOf<Medium>), 0, s, p);
-  else
+  else if (tiles == kTiny)
     hipLaunchKernelGGL((k_product<E, TERMS, EPI, Tiny, AO, BO>), dim3(grid_of<Tiny>(p)),
                        dim3(kThreadsOf<Tiny>), 0, s, p);
+  if constexpr (TERMS == 1)
+    if (tiles == kBrief)
+      hipLaunchKernelGGL((k_product<E, TERMS, EPI, Brief, AO, BO>), dim3(grid_of<Brief>(p)),
+                         dim3(kThreadsOf<Brief>), 0, s, p);
+  if constexpr (!BO)
+    if (tiles == kThin)
+      hipLaunchKernelGGL((k_product<E, TERMS, EPI, Thin, AO, BO>), dim3(grid_of<Thin>(p)),
+                         dim3(kThreadsOf<Thin>), 0, s, p);
 }
 
 unsigned blocks(int64_t threads, int cus) {
@@ -1129,7 +1171,11 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
 
   // the logits by pieces only where the weight's rows have to be copied
   const int64_t logits_piece = weight_fits ? V : l.piece;
-  const bool one_piece = l.piece >= V;
+  // the gradients by what a piece's gradients take, and its copy if there is one
+  const int64_t piece = weight_fits && V % kPad == 0
+                            ? std::min(l.ld_exps, std::max<int64_t>(256, l.room / l.pad / 256 * 256))
+                            : l.piece;
+  const bool one_piece = piece >= V;
   for (int64_t r0 = 0; r0 < R; r0 += l.chunk) {
     const int64_t n = std::min(l.chunk, R - r0);
     const Rows rows = rows_at(r0);
@@ -1160,7 +1206,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     a.exps = ws + l.exps;
     a.ld_exps = l.ld_exps;
     // (one kind of tile for all pieces: they share the rows of sums)
-    const Tiles tiles = choose(std::min(logits_piece, V), n, l.pitch_d, RATE, p->cus, 1).tiles;
+    const Tiles tiles = choose(std::min(logits_piece, V), n, l.pitch_d, RATE, p->cus, 1, true).tiles;
     for (int64_t v0 = 0; v0 < V; v0 += logits_piece) {
       const int64_t width = std::min(logits_piece, V - v0);
       // (a single piece's copy serves d_hidden as well)
@@ -1190,15 +1236,20 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     loss.epoch = epoch;
     const bool gradients = grad && (q->d_hidden || q->d_weight);
     const bool sum_later = way == kBoth && gradients && one_piece && loss.parts <= kFewParts;
-    if (way != kBackward && !sum_later)
-      hipLaunchKernelGGL(k_lse, dim3((unsigned)div_up(n, 16)), dim3(256), 0, s, loss);
+    if (way != kBackward && !sum_later) {
+      // few rows of many sums: more threads a row
+      if (n < 1024 && loss.parts > kFewParts)
+        hipLaunchKernelGGL(k_lse<64>, dim3((unsigned)div_up(n, 4)), dim3(256), 0, s, loss);
+      else
+        hipLaunchKernelGGL(k_lse<kShares>, dim3((unsigned)div_up(n, 256 / kShares)), dim3(256), 0, s, loss);
+    }
     if (!gradients) continue;
 
     // (of the first piece, the longest, which writes every part's sums)
-    const Choice for_h = choose(D, n, up(std::min(l.piece, V), kPad), RATE, p->cus, kMaxSplit);
+    const Choice for_h = choose(D, n, up(std::min(piece, V), kPad), RATE, p->cus, kMaxSplit, true);
     const int split = for_h.split;
-    for (int64_t v0 = 0; v0 < V; v0 += l.piece) {
-      const int64_t width = std::min(l.piece, V - v0);
+    for (int64_t v0 = 0; v0 < V; v0 += piece) {
+      const int64_t width = std::min(piece, V - v0);
       Grad g{};
       g.exps = a.exps;
       g.ld_exps = l.ld_exps;
@@ -1254,7 +1305,8 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       if (q->d_weight) {
         const bool first = r0 == 0, last = r0 + n == R;
         const bool direct = (first && last) || q->d_weight_dtype == SGB_F32;
-        tiles_w = choose(D, width, up(n, kPad), RATE, p->cus, 1).tiles;
+        w.steps = (int)div_up(n, kStepOf<E>);
+        tiles_w = !SPLIT && w.steps <= 16 ? kBrief : choose(D, width, up(n, kPad), RATE, p->cus, 1, false).tiles;
         w.a = xt.p;
         w.lda = xt.ld;
         w.plane_a = xt.plane;
@@ -1264,7 +1316,6 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
         w.M = D;
         w.N = width;
         w.cols_b = g.pitch;
-        w.steps = (int)(up(n, kPad) / kStepOf<E>);
         w.split = 1;
         w.most = most;
         w.scale = q->grad_scale / kBy;

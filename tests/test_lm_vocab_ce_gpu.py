@@ -116,6 +116,45 @@ def test_chunks_and_pieces(lm, dt, rows):
             test(o, c, above, 1.0, b)
 
 
+@pytest.mark.parametrize("V", [1 << 20, (1 << 20) + 77])
+@pytest.mark.parametrize("dt,rows", [("bf16", 1100), ("f16", 700), ("f32", 700)])
+def test_more_chunks(lm, dt, rows, V):
+    """Several chunks of rows with several pieces each, of a weight whose rows are
+    read where they are throughout and of one that takes copies."""
+    c = make(rows, 64, V, dt)
+    o, _ = run(lm, c)
+    test(o, c)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows", [1, 16, 17, 40, 100])
+def test_few_rows_of_whole_tiles(lm, rows, dt):
+    """Tiles for few rows, of a weight that is read where it is in every product."""
+    c = make(rows, 256, 32768, dt)
+    for way, above in (("loss_grad", None), ("split", torch.rand(rows, device="cuda") + 0.5)):
+        o, _ = run(lm, c, way, above)
+        test(o, c, above)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,D,V", [(1030, 64, 20000), (2100, 128, 9000), (500, 1088, 4000)])
+def test_short_sums(lm, rows, D, V, dt):
+    """Products whose summed dimension is short: few columns, few rows."""
+    c = make(rows, D, V, dt)
+    o, _ = run(lm, c)
+    test(o, c)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,D,V", [(33, 4096, 65600), (7, 16384, 20032)])
+def test_large_weight(lm, rows, D, V, dt):
+    """A weight of more than a piece's copies hold, whole steps long: it is read
+    where it is, and the gradients' pieces are longer than a copy's."""
+    c = make(rows, D, V, dt)
+    o, _ = run(lm, c)
+    test(o, c)
+
+
 def test_forward_in_chunks(lm):
     """Loss alone: the sums of exponentials take several chunks of rows."""
     rows, D, V = 2200, 8, (1 << 20) + 3
