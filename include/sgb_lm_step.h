@@ -40,16 +40,19 @@ extern "C" {
  *     d_hidden_r = sum_v g_rv w_v,   d_weight_v (+)= sum_r g_rv h_r.
  * Products of 16-bit types are summed in fp32; g (over grad_scale and the
  * row's factor, or the largest of these) is rounded to the operands' type for
- * the two products that follow.  fp32 operands are taken as three bf16 parts
- * each, and the six products of them that an fp32 result can tell.
+ * the two products that follow.  fp32 operands are multiplied as they are, or,
+ * where there are many rows, as three bf16 parts each and the six products of them
+ * that an fp32 result can tell.
  * A row whose logits are all -inf, or hold +inf or NaN, has NaN for its loss and
  * gradients, and so has d_weight if the row counts.  Of fp32 operands a row of h
- * or w that holds an infinity counts as one that holds a NaN.
+ * or w that holds an infinity may count as one that holds a NaN.
  * Weights and gradients from above have to be finite.
  *
- * The work goes by chunks of rows: the workspace does not grow past the
- * chunk's, about 1 GB for any number of rows (but for a 16-bit d_weight of more
- * than one chunk, 4 V D bytes for its sums).
+ * The work goes by chunks of rows: the workspace does not grow past a chunk's,
+ * at most 2 GiB of exponentials and 2.5 GiB of copies, gradients and sums.  A
+ * 16-bit d_weight of more than one chunk adds 4 V D bytes for its sums, and weight
+ * rows that may have to be copied, those of fp32 and of 16-bit elements whose D is
+ * no multiple of 8, their copy, up to 4 GiB.
  */
 typedef struct sgb_vocab_ce_s* sgb_vocab_ce;
 

@@ -1,25 +1,34 @@
 // lm_vocab_ce.hip -- cross-entropy of the head's product over a large
 // vocabulary, of libsgb_lm.so (formulas: include/sgb_lm_step.h).
 //
-// One product kernel, C = A B^T with both operands' rows along the summed
-// dimension, and five epilogues:
+// One product kernel, C = A B^T, and four epilogues:
 //   logits   A = weight rows, B = hidden rows: each wave leaves the largest of
-//            its logits and the sum of exponentials below it a token, and the
-//            exponentials themselves where gradients are to follow;
-//   d_hidden A = weight transposed, B = the logits' gradient;
-//   d_weight A = hidden transposed, B = the logits' gradient transposed.
+//            its logits and the sum of exponentials below it a token (kSums), and
+//            the exponentials themselves where gradients are to follow (kExps;
+//            kProbs, relative to a forward's lse);
+//   d_hidden A = the weight, B = the logits' gradient, summed over the vocabulary;
+//   d_weight A = hidden transposed, B = the logits' gradient, over the tokens
+//            (both kGrads).
 // The vocabulary, or the columns of the result, are A's rows: a lane holds four
 // neighbours of them for one of B's rows, so the softmax's sums stay in the
-// lane and the stores are of four elements.  The operands that have to be
-// transposed are copied piece by piece (a piece of the weight: 128 MB written
-// and read again from the last-level cache), and so are operands whose rows
-// are not whole 128-byte lines.
+// lane and the stores are of whole words.  An operand that is held the other way,
+// the weight for d_hidden and the logits' gradient for d_weight, is read
+// transposed from LDS by the instruction for it: a copy of it cost 105 us a
+// piece of 128 M elements.  What is copied are hidden rows (transposed for
+// d_weight, and where they end within a step) and weight rows that are no whole
+// words of 16 bytes.
 //
 // A chunk of tokens takes three products: its exponentials wait in 16 bits
 // (32 for fp16 and fp32 operands) for the row sums, since computing the logits
 // again would be a fourth.  They are relative to the largest of a wave's
 // columns and scaled by 2^15, so fp16 holds 11 bits of all that matter, and the
 // only rounding to the operands' type is that of the gradient itself.
+//
+// Bound by the matrix units where there are many tokens: 8192 tokens of 4096,
+// 131072 in the vocabulary, bf16: 19.9 to 20.3 ms for the loss and both
+// gradients, 1320 TFLOP/s, where a library product of such sizes reaches 1500;
+// the three products take 6.9, 6.5 and 6.4 ms, the rest 0.9.  Few tokens are
+// bound by the weight's traffic: the loss of 8 takes 187 us, 5.8 TB/s.
 
 #include <algorithm>
 #include <cmath>
@@ -71,7 +80,7 @@ struct Big {  // one workgroup a compute unit, for products that give each one
 struct BigOther : Big {  // fewer fragments of the operand that is read transposed
   static constexpr int WM = 64, WN = 128;
 };
-struct Medium {  // two, one at its start or end while the other multiplies
+struct Medium {  // two a compute unit, one at its start or end while the other multiplies
   static constexpr int TM = 128, TN = 128, WM = 64, WN = 64, kSteps = 1;
 };
 struct Tiny {  // for the time that loads take, not for how many there are
@@ -111,6 +120,9 @@ struct Product {
   int64_t M, N;              // rows of a, b; of an operand held the other way, columns,
   int64_t cols_a, cols_b;    // of which so many can be read
   int steps, split;          // of the summed dimension, over 1..steps workgroups
+  int last;                  // elements of a's last step that are the operand's: rows
+                             // that are no whole steps are read where they are
+  const char* end_a;         // what can be read of it
   int tm, tn;
   Rows rows;
   // logits
@@ -141,10 +153,11 @@ constexpr uint32_t kPartsB = 2u << 0 | 0u << 2 | 1u << 4 | 1u << 6 | 0u << 8 | 0
 // 1 KB a wave and load to consecutive addresses of LDS, from `base`, the same for
 // all lanes, and a lane's offset (a buffer's load: no addresses of 64 bits).
 template <int J>
-__device__ __forceinline__ void load_to_lds(const char* base, const uint32_t (&off)[J], char* lds) {
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t bytes, const uint32_t (&off)[J],
+                                            char* lds) {
 #ifdef __HIP_DEVICE_COMPILE__
   const __amdgpu_buffer_rsrc_t from =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, -1, 0x00027000);
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, (int)bytes, 0x00027000);
 #pragma unroll
   for (int j = 0; j < J; ++j)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -171,8 +184,8 @@ struct Stage {
       off[j] = (uint32_t)min((int64_t)row, left - 1) * (uint32_t)ld + part * 16;
     }
   }
-  __device__ __forceinline__ void load(const char* base, char* lds, int wave) const {
-    load_to_lds(base, off, lds + wave * J % kLoads * 1024);
+  __device__ __forceinline__ void load(const char* base, uint32_t bytes, char* lds, int wave) const {
+    load_to_lds(base, bytes, off, lds + wave * J % kLoads * 1024);
   }
 };
 
@@ -230,8 +243,8 @@ struct StageOther {
                (uint32_t)min((int64_t)part, left * (int)sizeof(E) / 16 - 1) * 16;
     }
   }
-  __device__ __forceinline__ void load(const char* base, char* lds, int wave) const {
-    load_to_lds(base, off, lds + wave * (J * 1024));
+  __device__ __forceinline__ void load(const char* base, uint32_t bytes, char* lds, int wave) const {
+    load_to_lds(base, bytes, off, lds + wave * (J * 1024));
   }
 };
 
@@ -309,6 +322,7 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
   constexpr int TM = C::TM, TN = C::TN, WM = C::WM, WN = C::WN;
   constexpr int WAVES = kThreadsOf<C> / 64, FM = WM / 16, FN = WN / 16;
   constexpr int kBytes = (TM + TN) * kRowBytes;
+  constexpr bool kCut = TERMS == 1 && !BO;  // a may end within a step
 
   // Workgroups go round the eight dies; each die gets a run of tiles of its
   // own, eight tiles of A by some of B at a time, whose operands its L2 shares.
@@ -336,6 +350,8 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
   const int to = (int)((int64_t)p.steps * (part + 1) / p.split);
   const int steps = (to - from) * TERMS, turns = (steps + C::kSteps - 1) / C::kSteps;
   int term = 0, step = from;
+  const uint32_t last_bytes = (uint32_t)min(
+      p.end_a - (a + (to - 1) * (AO ? kStepOf<E> * p.lda : (int64_t)kRowBytes)), (int64_t)UINT32_MAX);
   // The next steps' loads; past the last, that one's once more.  (A load that is
   // made only now and then makes the compiler wait for all of them.)
   const auto stage = [&](char* buf) {
@@ -347,9 +363,9 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
         pa += (kPartsA >> (2 * term) & 3) * p.plane_a;
         pb += (kPartsB >> (2 * term) & 3) * p.plane_b;
       }
-      sa.load(pa, buf + s * kBytes, wave);
-      sb.load(pb, buf + s * kBytes + TM * kRowBytes, wave);
       const bool wrap = step + 1 == to, on = !wrap || term + 1 < TERMS;
+      sa.load(pa, kCut && wrap ? last_bytes : UINT32_MAX, buf + s * kBytes, wave);
+      sb.load(pb, UINT32_MAX, buf + s * kBytes + TM * kRowBytes, wave);
       term += wrap && on;
       step = wrap ? (on ? from : step) : step + 1;
     }
@@ -421,6 +437,22 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
     if (kAll > kLead + kEach * kReads)
       __builtin_amdgcn_sched_group_barrier(0x008, kAll - kLead - kEach * kReads, 0);
   };
+  // What was read of a past its end (what follows it in memory, or nothing) is
+  // made zero, as b's is there.
+  const auto cut = [&](int kk, int s) {
+    if constexpr (kCut) {
+      const int most = from + s + 1 == p.steps ? p.last : kStepOf<E>;
+      const int left = most - (kk * kStepOf<E> / 2 + (lane >> 4) * (16 / (int)sizeof(E)));
+      typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+      U4 keep;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        keep[w] = sizeof(E) == 4 ? (left > w ? ~0u : 0u)
+                                 : (left > 2 * w + 1 ? ~0u : left > 2 * w ? 0xffffu : 0u);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[kk][i] = __builtin_bit_cast(V, __builtin_bit_cast(U4, fa[kk][i]) & keep);
+    }
+  };
   // a turn's steps but the last of their products
   const auto most = [&](const char* buf) {
     read(buf, 1);
@@ -441,8 +473,10 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
     for (int s = 1;; ++s) {
       all_loaded();
       read(buf0, 0);
+      cut(0, s - 1);
       multiply(0);
       read(buf0, 1);
+      cut(1, s - 1);
       multiply(1);
       if (s >= turns) break;
       __syncthreads();
@@ -472,13 +506,17 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
       multiply(1);
     }
     const char* buf = left > 1 ? buf1 : buf0;
+    int s = (turns - 1) * C::kSteps;
+    cut(0, s);
     most(buf);
-    for (int s = (turns - 1) * C::kSteps + 1; s < steps; ++s) {  // (none where a turn is one step)
+    for (++s; s < steps; ++s) {  // (none where a turn is one step)
       buf += kBytes;
       read(buf, 0);
       multiply(1);
+      cut(0, s);
       most(buf);
     }
+    cut(1, steps - 1);
     multiply(1);
   }
   all_loaded();  // LDS is free: no load to it is under way any more
@@ -789,7 +827,8 @@ __device__ __forceinline__ void finish_row(const Loss& q, int64_t r, float lse) 
 constexpr int kFewParts = 64;  // sums of a row that k_grad adds up itself
 constexpr int kShares = 16;  // of a row's sums, each added up alone and then in turn
 
-// 256 / SHARES rows a workgroup.
+// 256 / SHARES rows a workgroup.  (One row of 2048 sums: 25 us with 16 shares, 13
+// with 64.)
 template <int SHARES>
 __global__ __launch_bounds__(256) void k_lse(Loss q) {
   constexpr int kRows = 256 / SHARES;
@@ -951,7 +990,8 @@ namespace {
 
 constexpr int64_t kExpBytes = 1ll << 31;     // a chunk's exponentials
 constexpr int64_t kStatBytes = 1ll << 28;    // their sums
-constexpr int64_t kPieceElems = 1ll << 27;   // a piece's copies
+constexpr int64_t kPieceElems = 1ll << 27;   // a piece's gradients in the operands' type
+constexpr int64_t kCopyElems = 1ll << 31;    // the weight's copy
 constexpr int kMaxSplit = 32;
 
 int64_t up(int64_t n, int64_t to) { return div_up(n, to) * to; }
@@ -965,13 +1005,18 @@ enum Tiles { kBig, kMedium, kTiny, kThin, kBrief };
 int wave_cols_of(Tiles t) { return t == kBig ? Big::WM : t == kTiny ? Tiny::WM : Medium::WM; }
 
 // The tiles of a product, and among how many workgroups each tile's summed
-// dimension is shared out (up to `most`; their sums are then joined): what takes
-// the least time by what a round of workgroups was measured to take, a step and
-// beside the steps, in us: 256 x 256 tiles 1.65 and 8 (8192 x 32768 x 4096: 67% of
-// the matrix units' time), 128 x 128, two a compute unit, 1.05 and 2, 64 x 64
-// 0.39 and 4 (1021 x 1001 x 50021).  So 512 x 131072 logits of 4096 take 440 us in
-// the largest tiles and 570 in the next, 1021 x 50021 of 1001 130 and 117,
-// 2000 x 512 of 256 in three parts 24 with 128 x 128 tiles and 12 with 64 x 64.
+// dimension is shared out (their sums are then joined): what takes the least time
+// by what a round of workgroups, as many as a compute unit holds at once, was
+// measured to take, in us a step of 64 and beside the steps.  A gradient's tiles
+// leave more behind than the logits'.  Both sides, in us:
+//   loss, 512 tokens of 4096, 131072, bf16      Big 440, Medium 570
+//   logits, 1021 of 1001, 50021, fp16           Big 130, Medium 117
+//   logits, 512 of 256, 2000, fp32 in parts     Medium 24, Tiny 12
+//   loss, 8 tokens of 4096, 131072              Thin 187 bf16, 384 fp32; others 194, 629
+//   loss, 40 of the same, bf16                  Thin 281, Medium 198
+//   both gradients, 8, 300 and 1000 of the same Brief for d_weight 803, 1517, 2979,
+//     bf16                                      others 957, 1673, 3028
+//   forward and backward, 6272 of 64, 13617     Brief 244, others 276
 struct Choice {
   Tiles tiles;
   int split;
@@ -979,39 +1024,52 @@ struct Choice {
 };
 // 16-bit operands, fp32 in parts (six products of 16 bits), fp32 as it is.
 enum Rate { kHalf, kSplit, kWhole };
-Choice choose(int64_t M, int64_t N, int64_t K, Rate rate, int cus, int most, bool thin) {
-  const double per64[3][4] = {{1.65, 1.05, 0.39, 0.6}, {9.9, 6.3, 2.34, 3.6}, {14.0, 7.0, 1.0, 1.8}};
-  const double rest[4] = {8.0, 2.0, 4.0, 3.0};
-  const int64_t tiles[4] = {tiles_of<Big>(M, N), tiles_of<Medium>(M, N), tiles_of<Tiny>(M, N),
-                            tiles_of<Thin>(M, N)};
-  const int slots[4] = {cus, 2 * cus, cus, 2 * cus};
-  const int64_t steps = K / kPad;
+// For: the logits; a gradient; a gradient with B's rows held the other way.
+enum Use { kLogits, kGradient, kOther };
+Choice choose(int64_t M, int64_t N, int64_t K, Rate rate, int cus, Use use) {
+  const double per64[3][5] = {  // Big, Medium, Tiny, Thin, Brief
+      {1.65, 1.05, 0.39, 0.6, 2.3}, {9.9, 6.3, 2.34, 3.6, 0}, {14.0, 7.0, 1.0, 1.8, 15.0}};
+  const double rest[3][5] = {{8, 2, 4, 3, 2.5}, {21, 8, 4.5, 3, 10}, {25, 9, 5, 3, 9}};
+  const double* beside = rest[use == kLogits ? 0 : rate == kHalf ? 1 : 2];
+  const int64_t tiles[5] = {tiles_of<Big>(M, N), tiles_of<Medium>(M, N), tiles_of<Tiny>(M, N),
+                            tiles_of<Thin>(M, N), tiles_of<Brief>(M, N)};
+  const int at_once[5] = {1, 2, 1, 2, 4};
+  // (a round's time where a compute unit gets one workgroup)
+  const double alone[5] = {1, rate == kWhole ? 0.6 : 0.75, 1, 0.6, 0.5};
+  const int64_t steps = div_up(K, kPad);
+  const int most = use == kGradient ? kMaxSplit : 1;
   Choice best{kBig, 1, 1e300};
-  for (int t = 0; t < (thin && N <= Thin::TN ? 4 : 3); ++t)
-    for (int split = 1; split <= most && split <= steps; split *= 2) {
-      if (split > 1 && tiles[t] * split > 2 * cus) break;
-      double us = (double)div_up(tiles[t] * split, slots[t]) *
-                  ((double)div_up(steps, split) * per64[rate][t] + rest[t]);
+  for (int t = 0; t < 5; ++t) {
+    if (t == kThin && (use == kOther || N > Thin::TN)) continue;
+    if (t == kBrief && rate == kSplit) continue;
+    for (int split = 1; split <= most && split <= steps; ++split) {
+      const int64_t all = tiles[t] * split;
+      if (split > 1 && all > 2 * cus) break;
+      double us = std::max((double)div_up(all, cus) / at_once[t], alone[t]) *
+                  ((double)div_up(steps, split) * per64[rate][t] + beside[t]);
       if (split > 1) us += 4 + 2e-6 * (double)(M * N) * split;  // the sums written and read
       if (us < best.us) best = {(Tiles)t, split, us};
     }
+  }
   return best;
 }
 
 // fp32 operands in parts take less of the matrix units and have to be copied, at
-// 10 bytes an element and 4.5 TB/s: for few rows the copy costs more.
+// 10 bytes an element and 4.5 TB/s: for few rows the copy costs more.  Both
+// gradients, us in parts and as they are, tokens of 4096, 32000: 100 1293 and 848,
+// 300 2236 and 2135, 1000 4425 and 5716.
 bool in_parts(const sgb_vocab_ce_s* p, int64_t rows) {
   const double copy = (double)p->V * p->D * 10 / 4.5e6;
-  const int64_t K = up(p->D, kPad);
-  return choose(p->V, rows, K, kSplit, p->cus, 1, true).us + copy < choose(p->V, rows, K, kWhole, p->cus, 1, true).us;
+  return choose(p->V, rows, p->D, kSplit, p->cus, kLogits).us + copy <
+         choose(p->V, rows, p->D, kWhole, p->cus, kLogits).us;
 }
 
 // What a call lays out in its workspace.
 struct Layout {
   int parts;           // of an element
   int64_t chunk, pad;  // rows a chunk, rounded up for the summed dimension
-  int64_t piece;       // of the vocabulary, where its rows are copied
-  int64_t room;        // elements of a piece's gradients
+  int64_t piece;       // of the vocabulary, whose gradients are held
+  int64_t copied;      // and whose weight rows
   int64_t pitch_d, ld_exps;
   size_t lse, said, most, stats, x, xt, w, exps, plain, scaled, sums, dw, bytes;
 };
@@ -1024,12 +1082,16 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   l.ld_exps = up(V, 256);  // whole tiles
   int64_t most = kStatBytes / (l.ld_exps / Tiny::WM * 8);
   if (gradient) most = std::min(most, kExpBytes / (l.ld_exps * exp_size));
+  most = std::min(most, kPieceElems / l.pitch_d);  // of their copies and sums
   most = std::max<int64_t>(most / 256 * 256, 64);
   l.chunk = std::min(rows, most);
   l.pad = up(l.chunk, kPad);
-  const int64_t room = l.room = kPieceElems / l.parts;
-  l.piece = std::min(l.ld_exps,
-                     std::max<int64_t>(256, std::min(room / l.pad, room / l.pitch_d) / 256 * 256));
+  // Whole tiles.  Rows that are no whole words of 16 bytes are always copied, as
+  // parts are; others only if a stride or an address calls for it.
+  const int64_t room = kPieceElems / l.parts, size = dtype == SGB_F32 ? 4 : 2;
+  const int64_t copy_room = l.parts > 1 || D * size % 16 != 0 ? kCopyElems / l.parts : room;
+  l.piece = std::min(l.ld_exps, std::max<int64_t>(256, room / l.pad / 256 * 256));
+  l.copied = std::min(l.ld_exps, std::max<int64_t>(256, copy_room / l.pitch_d / 256 * 256));
   size_t at = kHeaderBytes;
   const auto take = [&](int64_t bytes) {
     const size_t here = at;
@@ -1042,8 +1104,7 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   l.most = take(4);
   l.stats = take(l.ld_exps / Tiny::WM * 8 * l.chunk);
   l.x = take(l.pad * l.pitch_d * part);
-  // a piece's weight rows
-  l.w = take(std::min(l.ld_exps, std::max<int64_t>(256, room / l.pitch_d)) * l.pitch_d * part);
+  l.w = take(l.copied * l.pitch_d * part);
   if (gradient) {
     l.xt = take(D * l.pad * part);
     l.exps = take(l.chunk * l.ld_exps * exp_size);
@@ -1068,7 +1129,6 @@ unsigned grid_of(Product& p) {
 
 template <typename E, int TERMS, int EPI, bool AO = false, bool BO = false>
 void product(Product p, Tiles tiles, hipStream_t s) {
-  if (TERMS == 1 && tiles == kMedium && p.steps <= 4) tiles = kBrief;
   if (tiles == kBig)
     hipLaunchKernelGGL((k_product<E, TERMS, EPI, typename std::conditional<AO, BigOther, Big>::type, AO, BO>),
                        dim3(grid_of<Big>(p)), dim3(kThreadsOf<Big>), 0, s, p);
@@ -1097,6 +1157,8 @@ enum Way { kForward, kBackward, kBoth };
 struct Operand {
   const char* p;
   int64_t ld, plane;  // bytes
+  const char* end;    // null: rows are whole steps, and as many
+  int64_t cols;
 };
 
 template <typename T, bool SPLIT>
@@ -1138,13 +1200,14 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
   };
   if (most) hipLaunchKernelGGL(k_most, dim3(1), dim3(1024), 0, s, rows_at(0), R, most);
 
-  // Rows as the products read them: whole 128-byte lines, 16-byte aligned, a
-  // tile's within 32 bits.
+  // Rows as the products read them: 16-byte aligned, a tile's within 32 bits; the
+  // hidden rows, whose ends are not cut, of whole steps.
   const auto fits = [&](const void* a, int64_t stride, int64_t rows) {
-    return !SPLIT && D % kPad == 0 && aligned(a, 16) &&
+    return !SPLIT && D * ES % 16 == 0 && aligned(a, 16) &&
            (rows < 2 || (stride * ES % 16 == 0 && stride * ES < (1 << 23)));
   };
   const bool weight_fits = fits(weight, q->weight_stride, V);
+  const bool weight_copied = !weight_fits && l.copied >= V;  // as a whole
   Copies<T, SPLIT> copies;
   const auto copy_of = [&](const T* src, int64_t stride, int64_t n) {
     Copy<T, SPLIT> c{src, stride, n, D};
@@ -1155,41 +1218,58 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     return c;
   };
   const auto operand = [](const E* p, const Copy<T, SPLIT>& c) {
-    return Operand{reinterpret_cast<const char*>(p), c.pitch * ES, c.plane * ES};
+    return Operand{reinterpret_cast<const char*>(p), c.pitch * ES, c.plane * ES, nullptr, c.pitch};
   };
-  // A piece of the weight; whole: its rows are read by whole steps, past the
-  // vocabulary where that is not one of steps.
-  const auto weight_rows = [&](int64_t v0, int64_t width, bool whole) {
-    const T* src = weight + v0 * q->weight_stride;
-    if (weight_fits && !(whole && v0 + width == V && V % kPad != 0))
-      return Operand{reinterpret_cast<const char*>(src), q->weight_stride * ES, 0};
-    Copy<T, SPLIT> c = copy_of(src, q->weight_stride, width);
+  Operand all{};
+  if (weight_fits) {
+    all = {reinterpret_cast<const char*>(weight), q->weight_stride * ES, 0,
+           reinterpret_cast<const char*>(weight + (V - 1) * q->weight_stride + D), D};
+  } else if (weight_copied) {
+    Copy<T, SPLIT> c = copy_of(weight, q->weight_stride, V);
+    c.to = elems(l.w);
+    copies.c[copies.n++] = c;
+    all = operand(c.to, c);
+  }
+  // a piece of the weight
+  const auto weight_rows = [&](int64_t v0, int64_t width) {
+    if (all.p) {
+      Operand o = all;
+      o.p += v0 * o.ld;
+      return o;
+    }
+    Copy<T, SPLIT> c = copy_of(weight + v0 * q->weight_stride, q->weight_stride, width);
     c.to = elems(l.w);
     copies.c[copies.n++] = c;
     return operand(c.to, c);
   };
+  const auto set_a = [&](Product& p, const Operand& o, int64_t K) {
+    p.a = o.p;
+    p.lda = o.ld;
+    p.plane_a = o.plane;
+    p.cols_a = o.cols;
+    p.end_a = o.end ? o.end : reinterpret_cast<const char*>(UINTPTR_MAX);
+    p.steps = (int)div_up(K, kStepOf<E>);
+    p.last = o.end ? (int)(K - (int64_t)(p.steps - 1) * kStepOf<E>) : kStepOf<E>;
+  };
 
-  // the logits by pieces only where the weight's rows have to be copied
-  const int64_t logits_piece = weight_fits ? V : l.piece;
-  // the gradients by what a piece's gradients take, and its copy if there is one
-  const int64_t piece = weight_fits && V % kPad == 0
-                            ? std::min(l.ld_exps, std::max<int64_t>(256, l.room / l.pad / 256 * 256))
-                            : l.piece;
+  // by pieces only where the weight's rows have to be copied so
+  const int64_t logits_piece = all.p ? V : std::min(l.copied, l.piece);
+  const int64_t piece = all.p ? l.piece : logits_piece;
   const bool one_piece = piece >= V;
   for (int64_t r0 = 0; r0 < R; r0 += l.chunk) {
     const int64_t n = std::min(l.chunk, R - r0);
     const Rows rows = rows_at(r0);
     const T* x = static_cast<const T*>(q->hidden) + r0 * q->hidden_stride;
     Copy<T, SPLIT> c = copy_of(x, q->hidden_stride, n);
-    Operand xo{reinterpret_cast<const char*>(x), q->hidden_stride * ES, 0}, xt{}, wo{};
-    if (!fits(x, q->hidden_stride, n)) {
+    Operand xo{reinterpret_cast<const char*>(x), q->hidden_stride * ES, 0, nullptr, D}, xt{}, wo{};
+    if (D % kPad != 0 || !fits(x, q->hidden_stride, n)) {
       c.to = elems(l.x);
       xo = operand(c.to, c);
     }
     if (grad && q->d_weight) {
       c.to_t = elems(l.xt);
       c.count = rows;
-      xt = {reinterpret_cast<const char*>(c.to_t), c.pitch_t * ES, c.plane_t * ES};
+      xt = {reinterpret_cast<const char*>(c.to_t), c.pitch_t * ES, c.plane_t * ES, nullptr, c.pitch_t};
     }
     if (c.to || c.to_t) copies.c[copies.n++] = c;
     Product a{};
@@ -1197,7 +1277,6 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     a.ldb = xo.ld;
     a.plane_b = xo.plane;
     a.N = a.tokens = n;
-    a.steps = (int)(l.pitch_d / kStepOf<E>);
     a.split = 1;
     a.rows = rows;
     a.stats = reinterpret_cast<float2*>(ws + l.stats);
@@ -1206,15 +1285,12 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     a.exps = ws + l.exps;
     a.ld_exps = l.ld_exps;
     // (one kind of tile for all pieces: they share the rows of sums)
-    const Tiles tiles = choose(std::min(logits_piece, V), n, l.pitch_d, RATE, p->cus, 1, true).tiles;
+    const Tiles tiles = choose(std::min(logits_piece, V), n, D, RATE, p->cus, kLogits).tiles;
     for (int64_t v0 = 0; v0 < V; v0 += logits_piece) {
       const int64_t width = std::min(logits_piece, V - v0);
-      // (a single piece's copy serves d_hidden as well)
-      wo = weight_rows(v0, width, grad && q->d_hidden && one_piece);
+      wo = weight_rows(v0, width);
       copies.launch(s);
-      a.a = wo.p;
-      a.lda = wo.ld;
-      a.plane_a = wo.plane;
+      set_a(a, wo, D);
       a.M = width;
       a.v0 = v0;
       if (way == kForward)
@@ -1246,7 +1322,18 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     if (!gradients) continue;
 
     // (of the first piece, the longest, which writes every part's sums)
-    const Choice for_h = choose(D, n, up(std::min(piece, V), kPad), RATE, p->cus, kMaxSplit, true);
+    const int64_t longest = std::min(piece, V);
+    const Tiles tiles_w = choose(D, longest, n, RATE, p->cus, kOther).tiles;
+    Choice for_h = choose(D, n, longest, RATE, p->cus, kGradient);
+    // Two products that leave compute units idle run side by side, d_hidden's sum
+    // shared out over those that d_weight leaves (512 tokens of 256, 2000, fp32: 16
+    // us, 24 shared out over all, 20 one after the other).
+    const bool together = q->d_hidden && q->d_weight && for_h.tiles == kTiny && tiles_w == kTiny;
+    const int idle = p->cus - (int)std::min<int64_t>(p->cus, tiles_of<Tiny>(D, longest));
+    if (together && idle > 0) {
+      const Choice fewer = choose(D, n, longest, RATE, idle, kGradient);
+      if (fewer.tiles == kTiny) for_h = fewer;
+    }
     const int split = for_h.split;
     for (int64_t v0 = 0; v0 < V; v0 += piece) {
       const int64_t width = std::min(piece, V - v0);
@@ -1273,20 +1360,16 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
         hipLaunchKernelGGL((k_grad<T, SPLIT, X, false>), grid, dim3(256), 0, s, g);
       Product h{}, w{};
       if (q->d_hidden) {
-        if (!one_piece) {
-          wo = weight_rows(v0, width, true);
+        if (!one_piece) {  // (a single piece's is there)
+          wo = weight_rows(v0, width);
           copies.launch(s);
         }
-        h.a = wo.p;
-        h.lda = wo.ld;
-        h.plane_a = wo.plane;
+        set_a(h, wo, width);
         h.b = static_cast<const char*>(kTwo ? g.plain : g.scaled);
         h.ldb = g.pitch * ES;
         h.plane_b = g.plane * ES;
         h.M = D;
-        h.cols_a = l.pitch_d;
         h.N = n;
-        h.steps = (int)(g.pitch / kStepOf<E>);
         h.split = std::min(split, h.steps);
         if (split == 1 && v0 + width == V) {
           h.rows = rows;
@@ -1301,15 +1384,10 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
           h.add = v0 > 0;
         }
       }
-      Tiles tiles_w = kBig;
       if (q->d_weight) {
         const bool first = r0 == 0, last = r0 + n == R;
         const bool direct = (first && last) || q->d_weight_dtype == SGB_F32;
-        w.steps = (int)div_up(n, kStepOf<E>);
-        tiles_w = !SPLIT && w.steps <= 16 ? kBrief : choose(D, width, up(n, kPad), RATE, p->cus, 1, false).tiles;
-        w.a = xt.p;
-        w.lda = xt.ld;
-        w.plane_a = xt.plane;
+        set_a(w, xt, n);
         w.b = static_cast<const char*>(g.scaled);
         w.ldb = g.pitch * ES;
         w.plane_b = g.plane * ES;
@@ -1333,8 +1411,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
           w.add = !first;
         }
       }
-      // two products that leave compute units idle run side by side
-      if (q->d_hidden && q->d_weight && for_h.tiles == kTiny && tiles_w == kTiny) {
+      if (together) {
         const unsigned first = grid_of<Tiny>(h), second = grid_of<Tiny>(w);
         hipLaunchKernelGGL((k_products<E, TERMS, Tiny>), dim3(first + second), dim3(kThreadsOf<Tiny>),
                            0, s, h, w, (int)first);

@@ -155,6 +155,17 @@ def test_large_weight(lm, rows, D, V, dt):
     test(o, c)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_chunks_of_long_rows(lm, dt):
+    """So many rows of so many columns that their copies take two chunks."""
+    rows, D, V = 8200, 16384, 70
+    c = make(rows, D, V, dt)
+    p = lm.VocabCrossEntropy(D, V)
+    assert p.workspace_bytes(2 * rows, DT[dt]) < p.workspace_bytes(rows, DT[dt]) * 1.01 + 16 * rows
+    o, _ = run(lm, c)
+    test(o, c)
+
+
 def test_forward_in_chunks(lm):
     """Loss alone: the sums of exponentials take several chunks of rows."""
     rows, D, V = 2200, 8, (1 << 20) + 3
@@ -196,6 +207,25 @@ def test_strides_and_alignment(lm, dt):
         for k in outs:
             assert torch.equal(outs[k][:, at:at + D], base[k]), (k, at, W)
             assert bool((outs[k][:, :at] == 5).all()) and bool((outs[k][:, at + D:] == 5).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,D,V", [(20, 8, 77), (70, 72, 1013), (5, 136, 20001), (600, 328, 3005)])
+def test_weight_rows_of_no_whole_steps(lm, rows, D, V, dt):
+    """Rows and a vocabulary that end within a step, the weight read where it is:
+    NaN behind each row and behind the last."""
+    c = make(rows, D, V, dt)
+    b = torch.full((V + 1, D + 24), float("nan"), dtype=DT[dt], device="cuda")
+    b[:V, :D] = c["weight"]
+    c["weight"] = b[:V, :D]
+    above = torch.rand(rows, device="cuda") + 0.5
+    base = None
+    for w in (c["weight"], c["weight"].contiguous()):
+        c["weight"] = w
+        o, _ = run(lm, c, "split", above)
+        test(o, c, above)
+        base = base or o
+        assert all(torch.equal(o[k], base[k]) for k in o)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
