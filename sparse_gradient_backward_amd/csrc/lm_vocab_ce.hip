@@ -1247,7 +1247,8 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     p.lda = o.ld;
     p.plane_a = o.plane;
     p.cols_a = o.cols;
-    p.end_a = o.end ? o.end : reinterpret_cast<const char*>(UINTPTR_MAX);
+    // (a copy's rows are whole steps; the difference to an address is signed)
+    p.end_a = o.end ? o.end : reinterpret_cast<const char*>(INTPTR_MAX);
     p.steps = (int)div_up(K, kStepOf<E>);
     p.last = o.end ? (int)(K - (int64_t)(p.steps - 1) * kStepOf<E>) : kStepOf<E>;
   };

@@ -166,6 +166,33 @@ def test_chunks_of_long_rows(lm, dt):
     test(o, c)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_large_weight_of_odd_address(lm, dt):
+    """A weight that begins at an odd element: its copy takes several pieces."""
+    rows, D, V = 33, 4096, 40003
+    c = make(rows, D, V, dt)
+    wide = torch.full((V, D + 8), float("nan"), dtype=DT[dt], device="cuda")
+    wide[:, 1:D + 1] = c["weight"]
+    c["weight"] = wide[:, 1:D + 1]
+    for way in ("loss_grad", "split"):
+        o, _ = run(lm, c, way)
+        test(o, c)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_far_apart(lm, dt):
+    """Rows further apart than 32 bits of bytes reach over a tile."""
+    rows, D, V, apart = 40, 64, 300, 1 << 22
+    c = make(rows, D, V, dt)
+    base, _ = run(lm, c)
+    for k, n in (("weight", V), ("hidden", rows)):
+        wide = torch.empty(n, apart, dtype=DT[dt], device="cuda")
+        wide[:, :D] = c[k]
+        o, _ = run(lm, {**c, k: wide[:, :D]})
+        test(o, c)
+        del wide
+
+
 def test_forward_in_chunks(lm):
     """Loss alone: the sums of exponentials take several chunks of rows."""
     rows, D, V = 2200, 8, (1 << 20) + 3
