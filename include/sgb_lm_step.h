@@ -40,7 +40,8 @@ extern "C" {
  *     d_hidden_r = sum_v g_rv w_v,   d_weight_v (+)= sum_r g_rv h_r.
  * Products of 16-bit types are summed in fp32; g (over grad_scale and the
  * row's factor, or the largest of these) is rounded to the operands' type for
- * the two products that follow.  fp32 operands are multiplied as they are, or,
+ * the two products that follow; in calls of up to 128 rows what that leaves is
+ * multiplied too.  fp32 operands are multiplied as they are, or,
  * where there are many rows, as three bf16 parts each and the six products of them
  * that an fp32 result can tell.
  * A row whose logits are all -inf, or hold +inf or NaN, has NaN for its loss and

@@ -22,7 +22,8 @@
 // (32 for fp16 and fp32 operands) for the row sums, since computing the logits
 // again would be a fourth.  They are relative to the largest of a wave's
 // columns and scaled by 2^15, so fp16 holds 11 bits of all that matter, and the
-// only rounding to the operands' type is that of the gradient itself.
+// only rounding to the operands' type is that of the gradient itself.  (Of few rows
+// what it leaves goes into the products as well.)
 //
 // Bound by the matrix units where there are many tokens: 8192 tokens of 4096,
 // 131072 in the vocabulary, bf16: 19.9 to 20.3 ms for the loss and both
@@ -863,6 +864,7 @@ struct Grad {
   // over the row's factor, and with it (over the largest); or null
   void *plain, *scaled;  // [up(tokens)][pitch]
   int64_t pitch, plane;
+  int64_t rest;      // elements to what the rounding left of each, or 0
 };
 
 // The gradient of a piece's logits from their exponentials, in the operands'
@@ -938,19 +940,28 @@ __global__ __launch_bounds__(256) void k_grad(Grad q) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       v[i] = on && i < n ? (e[i] * k - (label[u] == i ? 1.f : 0.f)) * kBy : 0.f;
-    const int64_t to = (r0 + lr) * q.pitch + c0 + c;
-    if (q.plain) store_parts<T, SPLIT>(v, static_cast<E*>(q.plain) + to, q.plane);
+    const auto store = [&](void* out) {
+      E* to = static_cast<E*>(out) + (r0 + lr) * q.pitch + c0 + c;
+      store_parts<T, SPLIT>(v, to, q.plane);
+      if (q.rest == 0) return;
+      float left[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) left[i] = v[i] - (float)(E)v[i];
+      store_parts<T, SPLIT>(left, to + q.rest, q.plane);
+    };
+    if (q.plain) store(q.plain);
     if (q.scaled) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= share;
-      store_parts<T, SPLIT>(v, static_cast<E*>(q.scaled) + to, q.plane);
+      store(q.scaled);
     }
   }
 }
 
 // d_hidden: the parts' sums in their order, the row's factor, one rounding.
 template <typename T>
-__global__ __launch_bounds__(256) void k_join(const float* sums, int split, int64_t rows, int D,
+__global__ __launch_bounds__(256) void k_join(const float* sums, int split, int64_t part_rows,
+                                              int64_t rows, int D,
                                               Rows count, bool scaled, float scale, T* out,
                                               int64_t stride) {
   const int64_t groups = (D + 7) / 8, all = rows * groups;
@@ -963,7 +974,7 @@ __global__ __launch_bounds__(256) void k_join(const float* sums, int split, int6
 #pragma unroll 4
       for (int s = 0; s < split; ++s) {
         float x[8];
-        widen8(load8(sums + ((int64_t)s * rows + r) * D + c, n), x);
+        widen8(load8(sums + (s * part_rows + r) * D + c, n), x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += x[i];
       }
@@ -998,6 +1009,14 @@ constexpr int64_t kStatBytes = 1ll << 28;    // their sums
 constexpr int64_t kPieceElems = 1ll << 27;   // a piece's gradients in the operands' type
 constexpr int64_t kCopyElems = 1ll << 31;    // the weight's copy
 constexpr int kMaxSplit = 32;
+
+// So few rows have room in the products' tiles for what the rounding of the logits'
+// gradient leaves, as further rows of d_hidden and a further stretch of d_weight's
+// sum.  (Of many rows the roundings average out, to sqrt(2) times the output's own;
+// of few one entry makes up a result, and it is up to twice.  Errors of 80 rows of
+// 2790, 2880 tokens, bf16: 0.0026 without, 0.0017 with; both gradients of 8 rows of
+// 4096, 131072 tokens, 737 and 848 us, of 60 756 and 864.)
+constexpr int64_t kFewRows = 128;
 
 int64_t up(int64_t n, int64_t to) { return div_up(n, to) * to; }
 
@@ -1093,9 +1112,10 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   l.pad = up(l.chunk, kPad);
   // Whole tiles.  Rows that are no whole words of 16 bytes are always copied, as
   // parts are; others only if a stride or an address calls for it.
+  const int64_t of_rows = l.parts > 1 ? l.pad : std::max(l.pad, std::min(2 * l.pad, 2 * kFewRows));
   const int64_t room = kPieceElems / l.parts, size = dtype == SGB_F32 ? 4 : 2;
   const int64_t copy_room = l.parts > 1 || D * size % 16 != 0 ? kCopyElems / l.parts : room;
-  l.piece = std::min(l.ld_exps, std::max<int64_t>(256, room / l.pad / 256 * 256));
+  l.piece = std::min(l.ld_exps, std::max<int64_t>(256, room / of_rows / 256 * 256));
   l.copied = std::min(l.ld_exps, std::max<int64_t>(256, copy_room / l.pitch_d / 256 * 256));
   size_t at = kHeaderBytes;
   const auto take = [&](int64_t bytes) {
@@ -1111,14 +1131,14 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   l.x = take(l.pad * l.pitch_d * part);
   l.w = take(l.copied * l.pitch_d * part);
   if (gradient) {
-    l.xt = take(D * l.pad * part);
+    l.xt = take(D * of_rows * part);
     l.exps = take(l.chunk * l.ld_exps * exp_size);
-    const int64_t grads = std::min(l.ld_exps * l.pad, std::max(room, 256 * l.pad)) * part;
+    const int64_t grads = std::min(l.ld_exps * of_rows, std::max(room, 256 * of_rows)) * part;
     l.scaled = take(grads);
     if (dtype == SGB_F16) l.plain = take(grads);
     // a split's sums for any fewer rows too: at most 2 cus tiles
     const int64_t shared = 2ll * p->cus * Big::TM * Big::TN / D + 1;
-    l.sums = take(std::max(l.chunk, std::min(kMaxSplit * l.chunk, shared)) * D * 4);
+    l.sums = take(std::max(of_rows, std::min(kMaxSplit * of_rows, shared)) * D * 4);
     if (rows > l.chunk && dtype != SGB_F32) l.dw = take(V * D * 4);
   }
   l.bytes = at;
@@ -1191,7 +1211,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
   constexpr float kBy = __is_same(T, f16_t) ? kUp : 1.f;
   const int64_t R = q->rows, V = p->V;
   const int D = p->D;
-  const bool grad = way != kForward;
+  const bool grad = way != kForward, rest = ES == 2 && !SPLIT && R <= kFewRows;
   const auto floats = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   const auto elems = [&](size_t o) { return reinterpret_cast<E*>(ws + o); };
   float* most = __is_same(T, f16_t) && grad && q->d_weight ? floats(l.most) : nullptr;
@@ -1218,7 +1238,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
     Copy<T, SPLIT> c{src, stride, n, D};
     c.pitch = l.pitch_d;
     c.plane = up(n, kPad) * c.pitch;
-    c.pitch_t = up(n, kPad);
+    c.pitch_t = up(n, kPad) * (rest ? 2 : 1);
     c.plane_t = D * c.pitch_t;
     return c;
   };
@@ -1278,6 +1298,12 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       xt = {reinterpret_cast<const char*>(c.to_t), c.pitch_t * ES, c.plane_t * ES, nullptr, c.pitch_t};
     }
     if (c.to || c.to_t) copies.c[copies.n++] = c;
+    if (rest && c.to_t) {
+      copies.launch(s);
+      c.to = nullptr;
+      c.to_t += up(n, kPad);
+      copies.c[copies.n++] = c;
+    }
     Product a{};
     a.b = xo.p;
     a.ldb = xo.ld;
@@ -1329,15 +1355,16 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
 
     // (of the first piece, the longest, which writes every part's sums)
     const int64_t longest = std::min(piece, V);
-    const Tiles tiles_w = choose(D, longest, n, RATE, p->cus, kOther).tiles;
-    Choice for_h = choose(D, n, longest, RATE, p->cus, kGradient);
+    const int64_t of = rest ? 2 * up(n, kPad) : n;  // rows of the logits' gradient
+    const Tiles tiles_w = choose(D, longest, of, RATE, p->cus, kOther).tiles;
+    Choice for_h = choose(D, of, longest, RATE, p->cus, kGradient);
     // Two products that leave compute units idle run side by side, d_hidden's sum
     // shared out over those that d_weight leaves (512 tokens of 256, 2000, fp32: 16
     // us, 24 shared out over all, 20 one after the other).
     const bool together = q->d_hidden && q->d_weight && for_h.tiles == kTiny && tiles_w == kTiny;
     const int idle = p->cus - (int)std::min<int64_t>(p->cus, tiles_of<Tiny>(D, longest));
     if (together && idle > 0) {
-      const Choice fewer = choose(D, n, longest, RATE, idle, kGradient);
+      const Choice fewer = choose(D, of, longest, RATE, idle, kGradient);
       if (fewer.tiles == kTiny) for_h = fewer;
     }
     const int split = for_h.split;
@@ -1354,6 +1381,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       g.width = width;
       g.pitch = up(width, kPad);
       g.plane = up(n, kPad) * g.pitch;
+      g.rest = rest ? g.plane : 0;
       // Both products take the gradient with the row's factor; but fp16 could not
       // hold that of a small one, and d_hidden takes it without.
       constexpr bool kTwo = __is_same(T, f16_t);
@@ -1375,9 +1403,9 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
         h.ldb = g.pitch * ES;
         h.plane_b = g.plane * ES;
         h.M = D;
-        h.N = n;
+        h.N = of;
         h.split = std::min(split, h.steps);
-        if (split == 1 && v0 + width == V) {
+        if (split == 1 && !rest && v0 + width == V) {
           h.rows = rows;
           h.by_row = kTwo ? kScaled : kKept;
           h.scale = q->grad_scale / kBy;
@@ -1393,7 +1421,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
       if (q->d_weight) {
         const bool first = r0 == 0, last = r0 + n == R;
         const bool direct = (first && last) || q->d_weight_dtype == SGB_F32;
-        set_a(w, xt, n);
+        set_a(w, xt, of);
         w.b = static_cast<const char*>(g.scaled);
         w.ldb = g.pitch * ES;
         w.plane_b = g.plane * ES;
@@ -1426,9 +1454,10 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
         if (q->d_weight) product<E, TERMS, kGrads, false, true>(w, tiles_w, s);
       }
     }
-    if (q->d_hidden && split > 1)
+    if (q->d_hidden && (split > 1 || rest))
       hipLaunchKernelGGL(k_join<T>, dim3(blocks(n * div_up(D, 8), p->cus)), dim3(256), 0, s,
-                         floats(l.sums), split, n, D, rows, (bool)__is_same(T, f16_t), q->grad_scale / kBy,
+                         floats(l.sums), rest ? 2 * split : split, rest ? up(n, kPad) : n, n, D, rows,
+                         (bool)__is_same(T, f16_t), q->grad_scale / kBy,
                          static_cast<T*>(q->d_hidden) + r0 * q->d_hidden_stride, q->d_hidden_stride);
   }
 }
