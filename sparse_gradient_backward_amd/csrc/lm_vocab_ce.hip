@@ -21,9 +21,10 @@
 // A chunk of tokens takes three products: its exponentials wait in 16 bits
 // (32 for fp16 and fp32 operands) for the row sums, since computing the logits
 // again would be a fourth.  They are relative to the largest of a wave's
-// columns and scaled by 2^15, so fp16 holds 11 bits of all that matter, and the
-// only rounding to the operands' type is that of the gradient itself.  (Of few rows
-// what it leaves goes into the products as well.)
+// columns (in a backward, the row's log-sum-exp) and scaled by 2^15, so fp16 holds 11
+// bits of all that matter but the label's, whose gradient is computed from its
+// logit, and the only rounding to the operands' type is that of the gradient itself.
+// (Of few rows what it leaves goes into the products as well.)
 //
 // Bound by the matrix units where there are many tokens: 8192 tokens of 4096,
 // 131072 in the vocabulary, bf16: 19.9 to 20.3 ms for the loss and both
@@ -583,6 +584,16 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
     } else {
       typedef typename std::conditional<__is_same(E, bf16_t) && TERMS == 1, f16_t, float>::type X;
       float top = 0.f, sum = 0.f;
+      if constexpr (EPI != kProbs || sizeof(X) == 2) {  // (k_grad takes it from 16 bits)
+        const int64_t label = there ? p.rows.labels[n] - (p.v0 + m0 + wm) : -1;
+        if (label >= 0 && label < WM && label + m0 + wm < p.M) {
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (label == 16 * i + 4 * (lane >> 4) + k) p.said[n] = acc[i][j][k];
+        }
+      }
       if constexpr (EPI == kProbs) {
         if (there) top = p.lse[n];
       } else {
@@ -592,14 +603,6 @@ __device__ __forceinline__ void product_tile(const Product& p, int block, char* 
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (mw + 16 * i + k >= p.M) acc[i][j][k] = -INFINITY;
-        }
-        const int64_t label = there ? p.rows.labels[n] - (p.v0 + m0 + wm) : -1;
-        if (label >= 0 && label < WM && label + m0 + wm < p.M) {
-#pragma unroll
-          for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (label == 16 * i + 4 * (lane >> 4) + k) p.said[n] = acc[i][j][k];
         }
         top = -INFINITY;
 #pragma unroll
@@ -868,7 +871,10 @@ struct Grad {
 };
 
 // The gradient of a piece's logits from their exponentials, in the operands'
-// type, zeros past the vocabulary and past the last token.
+// type, zeros past the vocabulary and past the last token.  Of exponentials that
+// waited in 16 bits the label's entry, p - 1, comes from its logit instead: where p
+// is near one, the rounding (2^-12, the half step below one) may be all of it.  (In
+// 32 bits it is 2^-25, less than the log-sum-exp's own.)
 template <typename T, bool SPLIT, typename X, bool SUM>
 __global__ __launch_bounds__(256) void k_grad(Grad q) {
   typedef typename Parts<T, SPLIT>::E E;
@@ -939,7 +945,14 @@ __global__ __launch_bounds__(256) void k_grad(Grad q) {
     widen8(raw[u], e);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      v[i] = on && i < n ? (e[i] * k - (label[u] == i ? 1.f : 0.f)) * kBy : 0.f;
+      v[i] = on && i < n ? (e[i] * k - (sizeof(X) == 4 && label[u] == i ? 1.f : 0.f)) * kBy : 0.f;
+    if (sizeof(X) == 2 && on && label[u] >= 0 && label[u] < n) {
+      const float less =
+          expm1f(q.rows.said[r0 + lr] - (SUM ? part[0][lr].x : lse[u])) * kBy;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (label[u] == i) v[i] = less;
+    }
     const auto store = [&](void* out) {
       E* to = static_cast<E*>(out) + (r0 + lr) * q.pitch + c0 + c;
       store_parts<T, SPLIT>(v, to, q.plane);
