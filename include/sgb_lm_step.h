@@ -146,8 +146,10 @@ sgb_status sgb_dropout_apply(sgb_dropout plan, const sgb_dropout_args* args, voi
  * to nearest even, clamped to +-M.  v comes from the unrounded x_out; all in fp32.
  * A group whose scale would be below 2^-126 has scale 0 and codes 0.  A group
  * that holds a NaN has scale NaN and codes 0; one with an infinity in h or x
- * has a NaN there (the row's other groups are 0).  A v past fp32's range (a
- * weight's doing) makes its group's scale infinite and its codes 0.
+ * has a NaN there (the row's other groups are 0).  A v or an x_out * weight past
+ * fp32's range (a weight's doing) makes its group's scale infinite and its codes
+ * 0.  A row whose squares' sum is past it has scale 0 and codes 0, as next to an
+ * infinity; one below 2^64 / sqrt(D) throughout has not.
  */
 typedef enum { SGB_CODE_INT8 = 0, SGB_CODE_E4M3 = 1 } sgb_code_kind;
 

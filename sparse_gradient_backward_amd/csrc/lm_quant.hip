@@ -58,21 +58,21 @@ __device__ __forceinline__ float fold_most(float v, int width) {
 // Codes are p * by, p = v * weight and by = M / (the largest p): 1 / rms cancels.
 // Every rounding on the way moves a few codes of those on the border between
 // two, so p keeps its rest, by is two floats, and only their sum is rounded.
+// Where the largest p is far from one, by or the rests would leave fp32's range:
+// p is then taken of v * up, a power of two, which is exact.
 struct Factor {
-  float hi, lo;
+  float hi, lo, up;
   bool on;
 };
 __device__ __forceinline__ Factor factor_of(float most_p, float scale, float M) {
-  Factor f{0.f, 0.f, scale > 0.f && scale < INFINITY};  // nor NaN
-  if (most_p > 0x1p-90f && most_p < 0x1p90f) {
+  Factor f{0.f, 0.f, 1.f, scale > 0.f && scale < INFINITY};  // nor NaN
+  if (f.on) {  // most_p > 0
+    f.up = most_p < 0x1p-64f ? 0x1p64f : most_p > 0x1p64f ? 0x1p-64f : 1.f;
+    most_p *= f.up;
     float r = __builtin_amdgcn_rcpf(most_p);
     r = fmaf(r, fmaf(-most_p, r, 1.f), r);
     f.hi = M * r;
     f.lo = fmaf(-most_p, f.hi, M) * r;
-  } else if (f.on) {
-    const double by = (double)M / (double)most_p;
-    f.hi = (float)by;
-    f.lo = (float)(by - (double)f.hi);
   }
   return f;
 }
@@ -187,6 +187,10 @@ __global__ __launch_bounds__(WIDE ? 512 : 256) void k_quant(Args a) {
           a.scales[r * a.ss + (a.in_group ? (in_row + k * a.tpr) / lanes : 0)] = scale;
       }
       if (!mine || n[k] <= 0) continue;
+      if (by.up != 1.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] *= by.up;
+      }
       float c[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
