@@ -13,8 +13,10 @@
  * plans and their devices, matrices with row strides, workspaces
  * (sgb_lm_device_status() reads theirs), no allocation, no memset and no host
  * wait in a call, no floating-point atomics.  Pointers need no more than their
- * element's alignment.  Rows may be 0: nothing is enqueued, but that a weight
- * gradient that is not accumulated is written as zeros.
+ * element's alignment.  An output, the workspace among them, that overlaps
+ * anything else of the call is refused, but where a line here allows it.  Rows
+ * may be 0: nothing is enqueued, but that a weight gradient that is not
+ * accumulated is written as zeros.
  */
 #ifndef SGB_LM_STEP_H
 #define SGB_LM_STEP_H
@@ -148,8 +150,8 @@ sgb_status sgb_dropout_apply(sgb_dropout plan, const sgb_dropout_args* args, voi
  * that holds a NaN has scale NaN and codes 0; one with an infinity in h or x
  * has a NaN there (the row's other groups are 0).  A v or an x_out * weight past
  * fp32's range (a weight's doing) makes its group's scale infinite and its codes
- * 0.  A row whose squares' sum is past it has scale 0 and codes 0, as next to an
- * infinity; one below 2^64 / sqrt(D) throughout has not.
+ * 0.  A row whose squares' sum is past it has codes 0 and scales 0, as next to an
+ * infinity (NaN where a product is past it too); none below 2^64 / sqrt(D) has.
  */
 typedef enum { SGB_CODE_INT8 = 0, SGB_CODE_E4M3 = 1 } sgb_code_kind;
 

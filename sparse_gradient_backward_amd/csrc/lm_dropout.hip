@@ -180,6 +180,8 @@ sgb_status sgb_dropout_apply(sgb_dropout p, const sgb_dropout_args* q, void* str
     return SGB_ERR_INVALID_ARGUMENT;
   if (!on_res && overlap(q->out, D, q->out_stride, eo, q->residual, D, q->residual_stride, eo, R))
     return SGB_ERR_INVALID_ARGUMENT;
+  if (overlap({q->out, R, D, q->out_stride, eo}, vector(q->state, 2, 8)))
+    return SGB_ERR_INVALID_ARGUMENT;
 
   Args a{};
   a.x = q->x;

@@ -371,4 +371,26 @@ inline bool overlap(const void* a, int64_t wa, int64_t sa, size_t ea, const void
   return !(d >= (uint64_t)wa * ea && d + (uint64_t)wb * eb <= pitch);
 }
 
+// An argument's elements: rows of `width` elements of `elem` bytes (a vector: one row).
+struct Extent {
+  const void* p;  // or null: not there
+  int64_t rows, width, stride;
+  size_t elem;
+};
+inline bool overlap(const Extent& a, const Extent& b) {
+  return overlap(a.p, a.width, a.stride, a.elem, b.p, b.width, b.stride, b.elem, a.rows, b.rows);
+}
+inline Extent vector(const void* p, int64_t n, size_t elem) { return {p, 1, n, n, elem}; }
+
+// Does any of `n` outputs share bytes with another, or with one of `m` inputs?
+inline bool any_overlap(const Extent* out, int n, const Extent* in, int m) {
+  for (int i = 0; i < n; ++i) {
+    for (int j = 0; j < m; ++j)
+      if (overlap(out[i], in[j])) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return true;
+  }
+  return false;
+}
+
 }  // namespace sgb_lm

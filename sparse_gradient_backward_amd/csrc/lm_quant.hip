@@ -301,11 +301,15 @@ sgb_status sgb_quant_norm_forward(sgb_quant_norm p, const sgb_quant_norm_args* q
   const bool on_x = q->x_out == q->x && (R < 2 || q->x_out_stride == q->x_stride);
   const bool on_h = q->x_out == q->h && q->res_dtype == q->dtype &&
                     (R < 2 || q->x_out_stride == q->h_stride);
-  if ((!on_x && overlap(q->x_out, D, q->x_out_stride, er, q->x, D, q->x_stride, er, R)) ||
-      (!on_h && overlap(q->x_out, D, q->x_out_stride, er, q->h, D, q->h_stride, e, R)) ||
-      overlap(q->q, D, q->q_stride, 1, q->h, D, q->h_stride, e, R) ||
-      overlap(q->q, D, q->q_stride, 1, q->x, D, q->x_stride, er, R) ||
-      overlap(q->q, D, q->q_stride, 1, q->x_out, D, q->x_out_stride, er, R))
+  // x_out may lie exactly on an input: the rest of what it may not touch
+  const Extent x_out{q->x_out, R, D, q->x_out_stride, er}, h{q->h, R, D, q->h_stride, e},
+      x{q->x, R, D, q->x_stride, er};
+  const Extent others[] = {{q->q, R, D, q->q_stride, 1},
+                           {q->scales, R, groups, q->scales_stride, 4},
+                           vector(q->stats, 4 * R, 4)};
+  const Extent read[] = {h, x, x_out, vector(q->weight, D, elem_size(q->weight_dtype))};
+  if ((!on_x && overlap(x_out, x)) || (!on_h && overlap(x_out, h)) || overlap(x_out, read[3]) ||
+      any_overlap(others, 3, read, 4))
     return SGB_ERR_INVALID_ARGUMENT;
 
   Args a{};

@@ -1506,19 +1506,29 @@ sgb_status call(sgb_vocab_ce p, const sgb_vocab_ce_args* q, Way way, void* ws, s
     if (way == kBackward && (!q->lse || !aligned(q->grad_loss, 4))) return SGB_ERR_INVALID_ARGUMENT;
     if (grad && q->d_hidden && !matrix_ok(q->d_hidden, D, q->d_hidden_stride, e))
       return SGB_ERR_INVALID_ARGUMENT;
-    if (grad) {
-      const size_t ew = elem_size(q->d_weight_dtype);
-      if (overlap(q->d_hidden, D, q->d_hidden_stride, e, q->hidden, D, q->hidden_stride, e, R) ||
-          overlap(q->d_hidden, D, q->d_hidden_stride, e, q->weight, D, q->weight_stride, e, R, V) ||
-          overlap(q->d_weight, D, q->d_weight_stride, ew, q->hidden, D, q->hidden_stride, e, V, R) ||
-          overlap(q->d_weight, D, q->d_weight_stride, ew, q->weight, D, q->weight_stride, e, V) ||
-          overlap(q->d_weight, D, q->d_weight_stride, ew, q->d_hidden, D, q->d_hidden_stride, e, V, R))
-        return SGB_ERR_INVALID_ARGUMENT;
-    }
     if (!workspace_ok(ws)) return SGB_ERR_INVALID_ARGUMENT;
   }
   const Layout l = layout(p, std::max<int64_t>(R, 1), q->dtype, grad);
-  if (R > 0 && ws_bytes < l.bytes) return SGB_ERR_WORKSPACE_TOO_SMALL;
+  if (R > 0) {
+    const bool back = way == kBackward;
+    const Extent none{};
+    const Extent lse = vector(q->lse, R, 4);
+    const Extent in[] = {{q->hidden, R, D, q->hidden_stride, e},
+                         {q->weight, V, D, q->weight_stride, e},
+                         vector(q->labels, R, 8),
+                         vector(q->row_weights, R, 4),
+                         back ? lse : none,
+                         back ? vector(q->grad_loss, R, 4) : none};
+    const Extent out[] = {
+        back ? none : vector(q->loss, R, 4),
+        back ? none : lse,
+        grad ? Extent{q->d_hidden, R, D, q->d_hidden_stride, e} : none,
+        grad && q->d_weight ? Extent{q->d_weight, V, D, q->d_weight_stride, elem_size(q->d_weight_dtype)}
+                            : none,
+        vector(ws, (int64_t)std::min(l.bytes, ws_bytes), 1)};
+    if (any_overlap(out, 5, in, 6)) return SGB_ERR_INVALID_ARGUMENT;
+    if (ws_bytes < l.bytes) return SGB_ERR_WORKSPACE_TOO_SMALL;
+  }
   DeviceGuard guard(p->device);
   if (!guard.ok) return SGB_ERR_HIP;
   if (R == 0) {
