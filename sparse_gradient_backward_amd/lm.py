@@ -124,14 +124,6 @@ def _int(name, v, lo, hi, where) -> int:
     return v
 
 
-def _finite(name, v, where) -> float:
-    """A number that a C float holds."""
-    v = float(v)
-    if not abs(v) <= 3.4028234663852886e38:
-        _bad(where, f"{name} must be finite in float32")
-    return v
-
-
 class _Handle:
     """Owns a plan handle of the C library, on the device current at creation."""
     _kind = ""
@@ -334,7 +326,7 @@ class TopkDistill(_Plan):
             self._vector("loss", loss, f32, rows, name),
             self._vector("stats", stats, f32, 4 * rows, name),
             self._vector("grad_loss", grad_loss, f32, rows, name), pg,
-            sl, si, sv, sg, rows, _DTYPE[dt], _finite("grad_scale", grad_scale, name))
+            sl, si, sv, sg, rows, _DTYPE[dt], grad_scale)
         ws, ws_bytes = self._space(workspace, name)
         _check(getattr(_lib, name)(self.handle, args, ws, ws_bytes,
                                    _stream(stream, self._index)), name)
@@ -471,8 +463,7 @@ class VocabCrossEntropy(_Plan):
             self._vector("row_weights", row_weights, f32, rows, name),
             self._vector("loss", loss, f32, rows, name), self._vector("lse", lse, f32, rows, name),
             self._vector("grad_loss", grad_loss, f32, rows, name), pdh, pdw,
-            sh, sw, sdh, sdw, rows, _DTYPE[dt], _DTYPE[wt], int(bool(accumulate)),
-            _finite("grad_scale", grad_scale, name))
+            sh, sw, sdh, sdw, rows, _DTYPE[dt], _DTYPE[wt], int(bool(accumulate)), grad_scale)
         ws, ws_bytes = self._space(workspace, name)
         _check(getattr(_lib, name)(self.handle, args, ws, ws_bytes,
                                    _stream(stream, self._index)), name)
