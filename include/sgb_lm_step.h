@@ -42,8 +42,11 @@ extern "C" {
  *     d_hidden_r = sum_v g_rv w_v,   d_weight_v (+)= sum_r g_rv h_r.
  * Products of 16-bit types are summed in fp32; g (over grad_scale and the
  * row's factor, or the largest of these) is rounded to the operands' type for
- * the two products that follow; in calls of up to 128 rows what that leaves is
- * multiplied too.  fp32 operands are multiplied as they are, or,
+ * the two products that follow: gradients are off by sqrt(2) times their own
+ * rounding where many rows average it.  What g's rounding leaves is multiplied
+ * too in calls of up to 128 rows, and in calls that ask for exact gradients: they
+ * are off by their own rounding alone, and these two products take twice as
+ * long.  fp32 operands are multiplied as they are, or,
  * where there are many rows, as three bf16 parts each and the six products of them
  * that an fp32 result can tell.
  * A row whose logits are all -inf, or hold +inf or NaN, has NaN for its loss and
@@ -64,9 +67,12 @@ sgb_status sgb_vocab_ce_create(sgb_vocab_ce* out, int32_t D, int64_t V);
 void sgb_vocab_ce_destroy(sgb_vocab_ce plan);
 
 /* For calls of up to `rows` rows (below 2^31) of that type; gradient: 0 for
- * forward alone, 1 for all of the calls. */
+ * forward alone, 1 for all of the calls but those for exact gradients, 2 for
+ * these too. */
 sgb_status sgb_vocab_ce_workspace_bytes(sgb_vocab_ce plan, int64_t rows, int32_t dtype,
                                         int32_t gradient, size_t* bytes);
+
+enum { SGB_VOCAB_CE_ACCUMULATE = 1, SGB_VOCAB_CE_EXACT = 2 };
 
 typedef struct {
   const void* hidden;               /* [rows][D], dtype                     */
@@ -84,7 +90,9 @@ typedef struct {
   int64_t rows;
   int32_t dtype;                    /* F32, BF16, F16                       */
   int32_t d_weight_dtype;           /* F32 or dtype                         */
-  int32_t accumulate;               /* 1: d_weight is added to              */
+  int32_t accumulate;               /* SGB_VOCAB_CE_ACCUMULATE: d_weight is
+                                       added to; SGB_VOCAB_CE_EXACT: exact
+                                       gradients, see above; or their sum   */
   float grad_scale;
 } sgb_vocab_ce_args;
 

@@ -24,7 +24,7 @@
 // columns (in a backward, the row's log-sum-exp) and scaled by 2^15, so fp16 holds 11
 // bits of all that matter but the label's, whose gradient is computed from its
 // logit, and the only rounding to the operands' type is that of the gradient itself.
-// (Of few rows what it leaves goes into the products as well.)
+// (Of few rows, or on demand, what it leaves goes into the products as well.)
 //
 // Bound by the matrix units where there are many tokens: 8192 tokens of 4096,
 // 131072 in the vocabulary, bf16: 19.9 to 20.3 ms for the loss and both
@@ -1026,7 +1026,8 @@ constexpr int kMaxSplit = 32;
 // So few rows have room in the products' tiles for what the rounding of the logits'
 // gradient leaves, as further rows of d_hidden and a further stretch of d_weight's
 // sum.  (Of many rows the roundings average out, to sqrt(2) times the output's own;
-// of few one entry makes up a result, and it is up to twice.  Errors of 80 rows of
+// of few one entry makes up a result, and it is up to twice.  More rows carry it if
+// the call asks for it, as rows and a stretch of tiles of their own.  Errors of 80 rows of
 // 2790, 2880 tokens, bf16: 0.0026 without, 0.0017 with; both gradients of 8 rows of
 // 4096, 131072 tokens, 737 and 848 us, of 60 756 and 864.)
 constexpr int64_t kFewRows = 128;
@@ -1111,7 +1112,7 @@ struct Layout {
   size_t lse, said, most, stats, x, xt, w, exps, plain, scaled, sums, dw, bytes;
 };
 
-Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
+Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient, bool exact) {
   Layout l{};
   l.parts = dtype == SGB_F32 ? 3 : 1;
   const int64_t V = p->V, D = p->D, exp_size = dtype == SGB_BF16 ? 2 : 4;
@@ -1125,7 +1126,9 @@ Layout layout(const sgb_vocab_ce_s* p, int64_t rows, int dtype, bool gradient) {
   l.pad = up(l.chunk, kPad);
   // Whole tiles.  Rows that are no whole words of 16 bytes are always copied, as
   // parts are; others only if a stride or an address calls for it.
-  const int64_t of_rows = l.parts > 1 ? l.pad : std::max(l.pad, std::min(2 * l.pad, 2 * kFewRows));
+  const int64_t of_rows = l.parts > 1 ? l.pad
+                          : exact     ? 2 * l.pad
+                                      : std::max(l.pad, std::min(2 * l.pad, 2 * kFewRows));
   const int64_t room = kPieceElems / l.parts, size = dtype == SGB_F32 ? 4 : 2;
   const int64_t copy_room = l.parts > 1 || D * size % 16 != 0 ? kCopyElems / l.parts : room;
   l.piece = std::min(l.ld_exps, std::max<int64_t>(256, room / of_rows / 256 * 256));
@@ -1224,7 +1227,8 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
   constexpr float kBy = __is_same(T, f16_t) ? kUp : 1.f;
   const int64_t R = q->rows, V = p->V;
   const int D = p->D;
-  const bool grad = way != kForward, rest = ES == 2 && !SPLIT && R <= kFewRows;
+  const bool grad = way != kForward, accumulate = q->accumulate & SGB_VOCAB_CE_ACCUMULATE;
+  const bool rest = ES == 2 && !SPLIT && (R <= kFewRows || q->accumulate & SGB_VOCAB_CE_EXACT);
   const auto floats = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   const auto elems = [&](size_t o) { return reinterpret_cast<E*>(ws + o); };
   float* most = __is_same(T, f16_t) && grad && q->d_weight ? floats(l.most) : nullptr;
@@ -1449,7 +1453,7 @@ void enqueue(const sgb_vocab_ce_s* p, const sgb_vocab_ce_args* q, Way way, const
                   v0 * q->d_weight_stride * elem_size(q->d_weight_dtype);
           w.ldo = q->d_weight_stride;
           w.out_dtype = q->d_weight_dtype;
-          w.add = q->accumulate || (direct && !first);
+          w.add = accumulate || (direct && !first);
           w.add_from = direct ? nullptr : floats(l.dw) + v0 * D;
         } else {
           w.out = floats(l.dw) + v0 * D;
@@ -1489,7 +1493,8 @@ sgb_status call(sgb_vocab_ce p, const sgb_vocab_ce_args* q, Way way, void* ws, s
   if (!float_dtype(q->dtype) || R < 0 || R >= (1ll << 31)) return SGB_ERR_INVALID_ARGUMENT;
   const size_t e = elem_size(q->dtype);
   if (grad) {
-    if (!std::isfinite(q->grad_scale) || (q->accumulate != 0 && q->accumulate != 1))
+    if (!std::isfinite(q->grad_scale) || q->accumulate < 0 ||
+        q->accumulate > (SGB_VOCAB_CE_ACCUMULATE | SGB_VOCAB_CE_EXACT))
       return SGB_ERR_INVALID_ARGUMENT;
     if (q->d_weight && ((q->d_weight_dtype != SGB_F32 && q->d_weight_dtype != q->dtype) ||
                         !matrix_ok(q->d_weight, D, q->d_weight_stride, elem_size(q->d_weight_dtype))))
@@ -1497,7 +1502,7 @@ sgb_status call(sgb_vocab_ce p, const sgb_vocab_ce_args* q, Way way, void* ws, s
     if (way == kBackward && !q->d_hidden && !q->d_weight) return SGB_ERR_INVALID_ARGUMENT;
   }
   hipStream_t s = reinterpret_cast<hipStream_t>(stream_);
-  if (R == 0 && (!grad || !q->d_weight || q->accumulate)) return SGB_OK;
+  if (R == 0 && (!grad || !q->d_weight || q->accumulate & SGB_VOCAB_CE_ACCUMULATE)) return SGB_OK;
   if (R > 0) {
     if (!matrix_ok(q->hidden, D, q->hidden_stride, e) || !matrix_ok(q->weight, D, q->weight_stride, e) ||
         !q->labels || !aligned(q->labels, 8) || !aligned(q->row_weights, 4) || !aligned(q->lse, 4))
@@ -1508,7 +1513,8 @@ sgb_status call(sgb_vocab_ce p, const sgb_vocab_ce_args* q, Way way, void* ws, s
       return SGB_ERR_INVALID_ARGUMENT;
     if (!workspace_ok(ws)) return SGB_ERR_INVALID_ARGUMENT;
   }
-  const Layout l = layout(p, std::max<int64_t>(R, 1), q->dtype, grad);
+  const Layout l = layout(p, std::max<int64_t>(R, 1), q->dtype, grad,
+                          grad && q->accumulate & SGB_VOCAB_CE_EXACT);
   if (R > 0) {
     const bool back = way == kBackward;
     const Extent none{};
@@ -1571,9 +1577,10 @@ void sgb_vocab_ce_destroy(sgb_vocab_ce p) { delete p; }
 
 sgb_status sgb_vocab_ce_workspace_bytes(sgb_vocab_ce p, int64_t rows, int32_t dtype,
                                         int32_t gradient, size_t* bytes) {
-  if (!p || !bytes || rows < 0 || rows >= (1ll << 31) || !float_dtype(dtype))
+  if (!p || !bytes || rows < 0 || rows >= (1ll << 31) || !float_dtype(dtype) || gradient < 0 ||
+      gradient > 2)
     return SGB_ERR_INVALID_ARGUMENT;
-  *bytes = layout(p, std::max<int64_t>(rows, 1), dtype, gradient != 0).bytes;
+  *bytes = layout(p, std::max<int64_t>(rows, 1), dtype, gradient != 0, gradient == 2).bytes;
   return SGB_OK;
 }
 

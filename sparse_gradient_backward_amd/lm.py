@@ -428,24 +428,27 @@ class VocabCrossEntropy(_Plan):
         self.V = _int("V", V, -2**63, 2**63, "VocabCrossEntropy")
         self._create(self.D, self.V)
 
-    def workspace_bytes(self, rows: int, dtype=torch.bfloat16, gradient: bool = True) -> int:
+    def workspace_bytes(self, rows: int, dtype=torch.bfloat16, gradient: bool = True,
+                        exact: bool = False) -> int:
         w = "sgb_vocab_ce_workspace_bytes"
         if dtype not in _DTYPE:
             _bad(w, "dtype must be float32, bfloat16 or float16")
         n = _sz()
         _check(_lib.sgb_vocab_ce_workspace_bytes(self.handle, _int("rows", rows, -2**63, 2**63, w),
-                                                 _DTYPE[dtype], int(bool(gradient)),
+                                                 _DTYPE[dtype], (1 + bool(exact)) * bool(gradient),
                                                  ctypes.byref(n)), w)
         return int(n.value)
 
-    def workspace(self, rows: int, dtype=torch.bfloat16, gradient: bool = True) -> torch.Tensor:
+    def workspace(self, rows: int, dtype=torch.bfloat16, gradient: bool = True,
+                  exact: bool = False) -> torch.Tensor:
         """A workspace for calls of up to `rows` rows of that type that follow
-        one another; without gradient for forward alone."""
-        return torch.empty(self.workspace_bytes(rows, dtype, gradient), dtype=torch.uint8,
+        one another; without gradient for forward alone, with exact for calls
+        for exact gradients as well."""
+        return torch.empty(self.workspace_bytes(rows, dtype, gradient, exact), dtype=torch.uint8,
                            device=self._device)
 
     def _call(self, name, hidden, weight, labels, loss, lse, grad_loss, d_hidden, d_weight,
-              grad_scale, accumulate, row_weights, workspace, stream):
+              grad_scale, accumulate, exact, row_weights, workspace, stream):
         if hidden.dtype not in _DTYPE:
             _bad(name, "hidden must be float32, bfloat16 or float16")
         dt, rows = hidden.dtype, hidden.shape[0]
@@ -463,7 +466,8 @@ class VocabCrossEntropy(_Plan):
             self._vector("row_weights", row_weights, f32, rows, name),
             self._vector("loss", loss, f32, rows, name), self._vector("lse", lse, f32, rows, name),
             self._vector("grad_loss", grad_loss, f32, rows, name), pdh, pdw,
-            sh, sw, sdh, sdw, rows, _DTYPE[dt], _DTYPE[wt], int(bool(accumulate)), grad_scale)
+            sh, sw, sdh, sdw, rows, _DTYPE[dt], _DTYPE[wt], bool(accumulate) + 2 * bool(exact),
+            grad_scale)
         ws, ws_bytes = self._space(workspace, name)
         _check(getattr(_lib, name)(self.handle, args, ws, ws_bytes,
                                    _stream(stream, self._index)), name)
@@ -474,23 +478,26 @@ class VocabCrossEntropy(_Plan):
         follow.  hidden [rows, D], weight [V, D] (of one type), labels [rows]
         int64 (negative: none), row_weights [rows] float32 or None."""
         self._call("sgb_vocab_ce_forward", hidden, weight, labels, loss, lse, None, None, None,
-                   0.0, False, row_weights, workspace, stream)
+                   0.0, False, False, row_weights, workspace, stream)
 
     def backward(self, hidden, weight, labels, lse, grad_loss=None, d_hidden=None, d_weight=None,
                  grad_scale: float = 1.0, accumulate: bool = False, row_weights=None,
-                 workspace=None, stream=None) -> None:
+                 workspace=None, stream=None, exact: bool = False) -> None:
         """d_hidden [rows, D] in hidden's type and d_weight [V, D] in weight's
         type or float32 (None: not wanted) of grad_scale * sum(grad_loss *
-        loss), from forward's lse; accumulate: d_weight is added to."""
+        loss), from forward's lse; accumulate: d_weight is added to; exact: of
+        16-bit types, the logits' gradient is multiplied with what its rounding
+        leaves, as it always is in calls of up to 128 rows: the gradients' error
+        is their own rounding alone, and their products take twice as long."""
         self._call("sgb_vocab_ce_backward", hidden, weight, labels, None, lse, grad_loss, d_hidden,
-                   d_weight, grad_scale, accumulate, row_weights, workspace, stream)
+                   d_weight, grad_scale, accumulate, exact, row_weights, workspace, stream)
 
     def loss_grad(self, hidden, weight, labels, loss, d_hidden=None, d_weight=None,
                   grad_scale: float = 1.0, accumulate: bool = False, lse=None, row_weights=None,
-                  workspace=None, stream=None) -> None:
+                  workspace=None, stream=None, exact: bool = False) -> None:
         """forward and backward (without grad_loss) in one go: one product less."""
         self._call("sgb_vocab_ce_loss_grad", hidden, weight, labels, loss, lse, None, d_hidden,
-                   d_weight, grad_scale, accumulate, row_weights, workspace, stream)
+                   d_weight, grad_scale, accumulate, exact, row_weights, workspace, stream)
 
 
 class Dropout(_Handle):
