@@ -12,7 +12,7 @@
 // Bound by memory: the generator runs while loads are in flight, four rows' at a
 // time.  32768 x 4096 bf16 with the residual: 140 us, 5.75 TB/s, where a long
 // elementwise product reaches 6.1; without it, the backward's form, 79 to 92 us;
-// 512 x 256 fp32 3.8.  Rows of fewer than eight columns are loaded one element at a
+// 512 x 256 fp32 3.6.  Rows of fewer than eight columns are loaded one element at a
 // time (no load of eight lies within such a row).
 
 #include <cmath>

@@ -27,10 +27,10 @@
 // (Of few rows, or on demand, what it leaves goes into the products as well.)
 //
 // Bound by the matrix units where there are many tokens: 8192 tokens of 4096,
-// 131072 in the vocabulary, bf16: 19.9 to 20.3 ms for the loss and both
-// gradients, 1320 TFLOP/s, where a library product of such sizes reaches 1500;
-// the three products take 6.9, 6.5 and 6.4 ms, the rest 0.9.  Few tokens are
-// bound by the weight's traffic: the loss of 8 takes 187 us, 5.8 TB/s.
+// 131072 in the vocabulary, bf16: 19.8 to 20.7 ms (cards differ) for the loss and
+// both gradients, 1275 to 1335 TFLOP/s, where a library product of such sizes
+// reaches 1500; the three products take 6.9, 6.5 and 6.4 ms, the rest 0.9.  Few
+// tokens are bound by the weight's traffic: the loss of 8 takes 185 us, 5.8 TB/s.
 
 #include <algorithm>
 #include <cmath>
@@ -258,8 +258,9 @@ __device__ __forceinline__ void all_loaded() {
   __syncthreads();
 }
 
-// LAST: what no kernel here reads again, non-temporally (both gradients of 8 rows of
-// 4096, 131072 tokens, bf16: 737 us so, 798 otherwise; of 8192 the same).
+// LAST: results, non-temporally: but for a d_weight or its sums that a later chunk
+// adds to, no kernel here reads them again (both gradients of 8 rows of 4096, 131072
+// tokens, bf16: 841 us so, 911 otherwise; of 300 1480 and 1522, of 8192 the same).
 template <typename T, bool LAST = false>
 __device__ __forceinline__ void store4(void* row, int64_t at, F4 v, int64_t n) {
   T* p = static_cast<T*>(row) + at;
@@ -1029,7 +1030,8 @@ constexpr int kMaxSplit = 32;
 // of few one entry makes up a result, and it is up to twice.  More rows carry it if
 // the call asks for it, as rows and a stretch of tiles of their own.  Errors of 80 rows of
 // 2790, 2880 tokens, bf16: 0.0026 without, 0.0017 with; both gradients of 8 rows of
-// 4096, 131072 tokens, 737 and 848 us, of 60 756 and 864.)
+// 4096, 131072 tokens, 734 and 841 us, of 60 754 and 859, of 300 1480 and 1988, of
+// 8192 20.5 and 34.8 ms.)
 constexpr int64_t kFewRows = 128;
 
 int64_t up(int64_t n, int64_t to) { return div_up(n, to) * to; }
@@ -1050,11 +1052,11 @@ int wave_cols_of(Tiles t) { return t == kBig ? Big::WM : t == kTiny ? Tiny::WM :
 //   loss, 512 tokens of 4096, 131072, bf16      Big 440, Medium 570
 //   logits, 1021 of 1001, 50021, fp16           Big 130, Medium 117
 //   logits, 512 of 256, 2000, fp32 in parts     Medium 24, Tiny 12
-//   loss, 8 tokens of 4096, 131072              Thin 187 bf16, 384 fp32; others 194, 629
+//   loss, 8 tokens of 4096, 131072              Thin 185 bf16, 373 fp32; others 194, 629
 //   loss, 40 of the same, bf16                  Thin 281, Medium 198
-//   both gradients, 8, 300 and 1000 of the same Brief for d_weight 803, 1517, 2979,
-//     bf16 (temporal stores)                    others 957, 1673, 3028
-//   forward and backward, 6272 of 64, 13617     Brief 244, others 276
+//   both gradients, 8, 300 and 1000 of the same Brief for d_weight 841, 1480, 3000,
+//     bf16                                      others 997, 1657, 2991
+//   forward and backward, 6272 of 64, 13617     Brief 251, others 288
 struct Choice {
   Tiles tiles;
   int split;
