@@ -68,7 +68,8 @@ struct Factor {
 __device__ __forceinline__ Factor factor_of(float most_p, float scale, float M) {
   Factor f{0.f, 0.f, 1.f, scale > 0.f && scale < INFINITY};  // nor NaN
   if (f.on) {  // most_p > 0
-    f.up = most_p < 0x1p-64f ? 0x1p64f : most_p > 0x1p64f ? 0x1p-64f : 1.f;
+    // (from 2^90 on: weights end at 2^128, so a v that matters stays a normal number)
+    f.up = most_p < 0x1p-64f ? 0x1p64f : most_p > 0x1p90f ? 0x1p-64f : 1.f;
     most_p *= f.up;
     float r = __builtin_amdgcn_rcpf(most_p);
     r = fmaf(r, fmaf(-most_p, r, 1.f), r);

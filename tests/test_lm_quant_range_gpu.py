@@ -81,3 +81,13 @@ def test_where_squares_and_products_leave_fp32(lm, D):
     norm.forward(h.cuda(), q, s)
     assert bool((s == torch.inf).all()) and not bool(q.any())
     check({"q": q.float()}, {"q": (torch.zeros(4, D).double(), torch.zeros(4, D).double())})
+
+
+@pytest.mark.parametrize("form", ["int8", "fp8"])
+@pytest.mark.parametrize("size", [1e-20, 2e-19, 1e-12, 1e-6])
+@pytest.mark.parametrize("D,group", [(300, 0), (4096, 0), (4096, 128)])
+def test_small_rows_under_the_largest_weights(lm, D, group, size, form):
+    """Products of ordinary size from both ends of the range, and large ones."""
+    h, _, w = rows_of(size, D, False)
+    w = w / w.abs().max() * 3e38
+    run(lm, h, None, w, form, group, f"size={size}")
